@@ -5,7 +5,8 @@ device pointers (ints), sizes, leading dimensions and a stream handle (int,
 0 = null stream). All arithmetic runs in the HIP kernels of the library; if
 the library is missing or cannot be loaded, every call raises.
 
-``matmul_f32`` / ``matmul_bf16`` are conveniences that take torch CUDA
+``matmul_f32`` / ``matmul_bf16``, ``quantize_fp8`` / ``matmul_fp8`` and
+``matmul_bf16_grouped`` / ``grouped_wgrad`` are conveniences that take torch CUDA
 tensors (row-major, unit column stride), pass their pointers, strides and
 torch's current stream, and raise ``GemmError`` on a non-zero status.
 """
@@ -44,7 +45,9 @@ OP_T = 1
 EXPORTS = ("gemm_f32", "gemm_bf16", "gemm_f32_ex", "gemm_bf16_ex", "gemm_bf16_ws",
            "gemm_bf16_workspace_size", "gemm_bf16_ws_noalloc", "gemm_f32_ws", "gemm_f32_workspace_size",
            "gemm_f32_bias_act", "gemm_bf16_bias_act", "gemm_f32_op", "gemm_bf16_op",
-           "gemm_f32_scaled", "gemm_bf16_scaled", "gemm_plan",
+           "gemm_f32_scaled", "gemm_bf16_scaled", "gemm_fp8_quantize_bf16",
+           "gemm_fp8_quantize_f32", "gemm_fp8", "gemm_bf16_grouped", "gemm_bf16_grouped_wgrad",
+           "gemm_bf16_grouped_wgrad_f32", "gemm_plan",
            "gemm_status_string")
 
 _lib = None
@@ -103,6 +106,19 @@ def _bind(path: str) -> ctypes.CDLL:
     for name in ("gemm_bf16_workspace_size", "gemm_f32_workspace_size"):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = ctypes.c_size_t, [i64, i64, i64]
+    for name in ("gemm_fp8_quantize_bf16", "gemm_fp8_quantize_f32"):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = ci, [ci, ci, i64, i64, vp, i64, vp, i64, vp, i64, vp]
+    lib.gemm_fp8.restype = ci
+    lib.gemm_fp8.argtypes = [i64, i64, i64, f32, vp, i64, vp, i64, vp, i64, vp, i64, ci, f32, vp,
+                             i64, vp, ci, vp]
+    lib.gemm_bf16_grouped.restype = ci
+    lib.gemm_bf16_grouped.argtypes = [ci, i64, i64, i64, i64, f32, vp, i64, vp, i64, i64, f32, vp,
+                                      i64, vp, vp, vp, i64, ci, vp]
+    for name in ("gemm_bf16_grouped_wgrad", "gemm_bf16_grouped_wgrad_f32"):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = ci, [i64, i64, i64, i64, f32, vp, i64, vp, i64, f32, vp, i64, i64,
+                                       vp, vp]
     lib.gemm_plan.restype = ci
     lib.gemm_plan.argtypes = [ci, i64, i64, i64, f32, vp, i64, vp, i64, f32, vp, i64, ci]
     lib.gemm_status_string.restype = ctypes.c_char_p
@@ -190,6 +206,38 @@ def gemm_bf16_scaled(opa, opb, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, row
                                    stream)
 
 
+def gemm_fp8_quantize_bf16(op, block_rows, rows, cols, X, ldx, Q, ldq, S, lds, stream=0) -> int:
+    return load().gemm_fp8_quantize_bf16(op, block_rows, rows, cols, X, ldx, Q, ldq, S, lds, stream)
+
+
+def gemm_fp8_quantize_f32(op, block_rows, rows, cols, X, ldx, Q, ldq, S, lds, stream=0) -> int:
+    return load().gemm_fp8_quantize_f32(op, block_rows, rows, cols, X, ldx, Q, ldq, S, lds, stream)
+
+
+def gemm_fp8(M, N, K, alpha, A, lda, SA, ldsa, B, ldb, SB, ldsb, b_block_rows, beta, C, ldc,
+             bias=None, act=0, stream=0) -> int:
+    return load().gemm_fp8(M, N, K, alpha, A, lda, SA, ldsa, B, ldb, SB, ldsb, b_block_rows, beta,
+                           C, ldc, bias, act, stream)
+
+
+def gemm_bf16_grouped(opb, groups, M, N, K, alpha, A, lda, B, ldb, strideb, beta, C, ldc, offsets,
+                      row_scale=None, bias=None, stridebias=0, act=0, stream=0) -> int:
+    return load().gemm_bf16_grouped(opb, groups, M, N, K, alpha, A, lda, B, ldb, strideb, beta, C,
+                                    ldc, offsets, row_scale, bias, stridebias, act, stream)
+
+
+def gemm_bf16_grouped_wgrad(groups, M, N, K, alpha, X, ldx, dY, lddy, beta, dW, lddw, stridedw,
+                            offsets, stream=0) -> int:
+    return load().gemm_bf16_grouped_wgrad(groups, M, N, K, alpha, X, ldx, dY, lddy, beta, dW, lddw,
+                                          stridedw, offsets, stream)
+
+
+def gemm_bf16_grouped_wgrad_f32(groups, M, N, K, alpha, X, ldx, dY, lddy, beta, dW, lddw, stridedw,
+                                offsets, stream=0) -> int:
+    return load().gemm_bf16_grouped_wgrad_f32(groups, M, N, K, alpha, X, ldx, dY, lddy, beta, dW,
+                                              lddw, stridedw, offsets, stream)
+
+
 def gemm_plan(elem_bytes, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, variant=0) -> int:
     return load().gemm_plan(elem_bytes, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, variant)
 
@@ -243,3 +291,111 @@ def matmul_bf16(A, B, C, alpha: float = 1.0, beta: float = 0.0, variant: int = V
                 stream=None) -> None:
     """C <- alpha * A @ B + beta * C for bf16 CUDA tensors (fp32 accumulation)."""
     _matmul("bf16", A, B, C, alpha, beta, variant, stream)
+
+
+def _want(name: str, t, dtypes, dim: int, shape=None) -> None:
+    """Check one operand: a tensor of one of `dtypes` on the current GPU, with
+    `dim` dimensions, the last with unit stride, and the given shape (None
+    entries are free)."""
+    import torch
+    if not t.is_cuda or t.dtype not in dtypes:
+        raise TypeError(f"{name} must be a CUDA tensor of dtype {' or '.join(map(str, dtypes))}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    if t.dim() != dim or (shape is not None and
+                          any(w is not None and w != s for w, s in zip(shape, t.shape))):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: expected unit stride in the last dimension")
+    if dim >= 2 and t.shape[-2] > 1 and t.stride(-2) < t.shape[-1]:
+        raise ValueError(f"{name}: its rows overlap")
+
+
+def _ld2(t) -> int:
+    """Leading dimension of the matrix in t's last two dimensions."""
+    return max(t.stride(-2) if t.shape[-2] > 1 else t.shape[-1], t.shape[-1], 1)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check(status: int) -> None:
+    if status != GEMM_OK:
+        raise GemmError(status)
+
+
+def quantize_fp8(X, Q, S, op: int = OP_N, block_rows: int = 1, stream=None) -> None:
+    """Quantise a bf16 or fp32 matrix (op OP_T: its transpose) into e4m3 values
+    Q (uint8 or float8_e4m3fn) and fp32 scales S, ceil(k / 128) x
+    ceil(rows / block_rows) for a Q of rows x k."""
+    import torch
+    _want("X", X, (torch.bfloat16, torch.float32), 2)
+    rows, cols = X.shape
+    r, k = (cols, rows) if op == OP_T else (rows, cols)
+    _want("Q", Q, (torch.uint8, torch.float8_e4m3fn), 2, (r, k))
+    _want("S", S, (torch.float32,), 2, (-(-k // 128), -(-r // max(int(block_rows), 1))))
+    fn = gemm_fp8_quantize_bf16 if X.dtype == torch.bfloat16 else gemm_fp8_quantize_f32
+    _check(fn(int(op), int(block_rows), rows, cols, X.data_ptr(), _ld2(X), Q.data_ptr(), _ld2(Q),
+              S.data_ptr(), _ld2(S), _stream_handle(stream)))
+
+
+def matmul_fp8(A, SA, B, SB, C, alpha: float = 1.0, beta: float = 0.0, b_block_rows: int = 128,
+               bias=None, act: int = ACT_NONE, stream=None) -> None:
+    """C <- act(alpha * (A SA) (B SB)^T + bias) + beta * C: A (M x K) and B
+    (N x K) in e4m3 with their scales, as quantize_fp8 makes them (A with
+    block_rows 1, B with b_block_rows), C in bf16."""
+    import torch
+    e4m3 = (torch.uint8, torch.float8_e4m3fn)
+    _want("A", A, e4m3, 2)
+    M, K = A.shape
+    _want("B", B, e4m3, 2, (None, K))
+    N, nk = B.shape[0], -(-K // 128)
+    _want("SA", SA, (torch.float32,), 2, (nk, M))
+    _want("SB", SB, (torch.float32,), 2, (nk, -(-N // max(int(b_block_rows), 1))))
+    _want("C", C, (torch.bfloat16,), 2, (M, N))
+    if bias is not None:
+        _want("bias", bias, (torch.bfloat16,), 1, (N,))
+    _check(gemm_fp8(M, N, K, float(alpha), A.data_ptr(), _ld2(A), SA.data_ptr(), _ld2(SA),
+                    B.data_ptr(), _ld2(B), SB.data_ptr(), _ld2(SB), int(b_block_rows), float(beta),
+                    C.data_ptr(), _ld2(C), _ptr(bias), int(act), _stream_handle(stream)))
+
+
+def matmul_bf16_grouped(A, B, C, offsets, opb: int = OP_N, alpha: float = 1.0, beta: float = 0.0,
+                        row_scale=None, bias=None, act: int = ACT_NONE, stream=None) -> None:
+    """Rows offsets[e] .. offsets[e + 1] - 1 of A (M x K) times B[e] (K x N, or
+    with opb OP_T its transpose, B[e] N x K) into the same rows of C (M x N),
+    with optional row scales (M, fp32) and biases (groups x N)."""
+    import torch
+    bf16 = (torch.bfloat16,)
+    _want("A", A, bf16, 2)
+    M, K = A.shape
+    _want("B", B, bf16, 3, (None, None, K) if opb == OP_T else (None, K, None))
+    E, N = B.shape[0], B.shape[1] if opb == OP_T else B.shape[2]
+    _want("C", C, bf16, 2, (M, N))
+    _want("offsets", offsets, (torch.int32,), 1, (E + 1,))
+    if row_scale is not None:
+        _want("row_scale", row_scale, (torch.float32,), 1, (M,))
+    if bias is not None:
+        _want("bias", bias, bf16, 2, (E, N))
+    _check(gemm_bf16_grouped(int(opb), E, M, N, K, float(alpha), A.data_ptr(), _ld2(A), B.data_ptr(),
+                             _ld2(B), B.stride(0), float(beta), C.data_ptr(), _ld2(C),
+                             offsets.data_ptr(), _ptr(row_scale), _ptr(bias),
+                             0 if bias is None else bias.stride(0), int(act),
+                             _stream_handle(stream)))
+
+
+def grouped_wgrad(X, dY, dW, offsets, alpha: float = 1.0, beta: float = 0.0, stream=None) -> None:
+    """dW[e] <- alpha * X_e^T dY_e + beta * dW[e] over the rows of each group:
+    X (M x K) and dY (M x N) in bf16, dW (groups x K x N) in bf16 or fp32."""
+    import torch
+    _want("X", X, (torch.bfloat16,), 2)
+    M, K = X.shape
+    _want("dY", dY, (torch.bfloat16,), 2, (M, None))
+    N = dY.shape[1]
+    _want("dW", dW, (torch.bfloat16, torch.float32), 3, (None, K, N))
+    E = dW.shape[0]
+    _want("offsets", offsets, (torch.int32,), 1, (E + 1,))
+    fn = gemm_bf16_grouped_wgrad if dW.dtype == torch.bfloat16 else gemm_bf16_grouped_wgrad_f32
+    _check(fn(E, M, N, K, float(alpha), X.data_ptr(), _ld2(X), dY.data_ptr(), _ld2(dY), float(beta),
+              dW.data_ptr(), _ld2(dW), dW.stride(0), offsets.data_ptr(), _stream_handle(stream)))

@@ -503,3 +503,165 @@ const char* gemm_status_string(int status) {
 }
 
 }  // extern "C"
+
+// ---- 8-bit operands and products grouped by expert -----------------------------
+
+namespace {
+
+bool size_ok(int64_t x) { return x >= 0 && x <= INT_MAX; }
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Status of the launch on the current device.
+template <typename F>
+gemm_status_t on_device(F&& launch) {
+    int cus = kFullCus;
+    const gemm_status_t dev = check_device(&cus);
+    if (dev != GEMM_OK) return dev;
+    return launch(cus) == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+template <typename T>
+gemm_status_t quantize(int op, int block_rows, int64_t rows, int64_t cols, const T* X, int64_t ldx, uint8_t* Q,
+                       int64_t ldq, float* S, int64_t lds, void* stream) {
+    if (!valid_op(op) || (block_rows != 1 && block_rows != dg::kScaleBlock)) return GEMM_ERR_INVALID_VALUE;
+    if (!size_ok(rows) || !size_ok(cols)) return GEMM_ERR_INVALID_VALUE;
+    const bool t = op == GEMM_OP_T;
+    const int64_t qr = t ? cols : rows, qc = t ? rows : cols;
+    if (ldx < max1(cols) || ldq < max1(qc) || lds < max1(ceil_div(qr, block_rows))) return GEMM_ERR_INVALID_VALUE;
+    if (!span_ok(sizeof(T), rows, cols, ldx) || !span_ok(1, qr, qc, ldq) ||
+        !span_ok(4, ceil_div(qc, dg::kScaleBlock), ceil_div(qr, block_rows), lds))
+        return GEMM_ERR_INVALID_VALUE;
+    if (!aligned(X, sizeof(T)) || !aligned(S, 4)) return GEMM_ERR_INVALID_VALUE;
+    if (rows == 0 || cols == 0) return GEMM_OK;
+    if (X == nullptr || Q == nullptr || S == nullptr) return GEMM_ERR_INVALID_VALUE;
+    const dg::QuantArgs<T> a{t, block_rows, rows, cols, X, ldx, Q, ldq, S, lds};
+    return on_device([&](int) { return dg::launch_quantize(a, reinterpret_cast<hipStream_t>(stream)); });
+}
+
+gemm_status_t grouped_wgrad(bool f32, int64_t groups, int64_t M, int64_t N, int64_t K, float alpha, const uint16_t* X,
+                            int64_t ldx, const uint16_t* dY, int64_t lddy, float beta, void* dW, int64_t lddw,
+                            int64_t stridedw, const int32_t* offsets, void* stream) {
+    const int esz = f32 ? 4 : 2;
+    if (!size_ok(groups) || !size_ok(M) || !size_ok(N) || !size_ok(K)) return GEMM_ERR_INVALID_VALUE;
+    if (ldx < max1(K) || lddy < max1(N) || lddw < max1(N)) return GEMM_ERR_INVALID_VALUE;
+    if (!span_ok(2, M, K, ldx) || !span_ok(2, M, N, lddy) || !span_ok(esz, K, N, lddw)) return GEMM_ERR_INVALID_VALUE;
+    const int64_t one = K > 0 ? (K - 1) * lddw + N : 0;
+    if (groups > 1 && (stridedw < one || !span_ok(esz, groups, one, stridedw))) return GEMM_ERR_INVALID_VALUE;
+    if (!aligned(X, 2) || !aligned(dY, 2) || !aligned(dW, esz) || !aligned(offsets, 4)) return GEMM_ERR_INVALID_VALUE;
+    if (groups == 0 || N == 0 || K == 0) return GEMM_OK;
+    const bool product = M > 0 && alpha != 0.f;
+    if (!product && beta == 1.f) return GEMM_OK;
+    if (dW == nullptr || offsets == nullptr) return GEMM_ERR_INVALID_VALUE;
+    if (product && (X == nullptr || dY == nullptr)) return GEMM_ERR_INVALID_VALUE;
+    dg::GroupedArgs a{};
+    a.wgrad = true;
+    a.groups = (int)groups;
+    a.M = product ? M : 0; a.N = N; a.K = K;
+    a.alpha = alpha; a.beta = beta;
+    a.A = X; a.lda = ldx;
+    a.B = dY; a.ldb = lddy;
+    a.C = dW; a.ldc = lddw; a.stridec = stridedw;
+    a.offsets = offsets;
+    a.f32 = f32;
+    return on_device([&](int cus) { return dg::launch_grouped(a, cus, reinterpret_cast<hipStream_t>(stream)); });
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_fp8_quantize_bf16(int op, int block_rows, int64_t rows, int64_t cols, const uint16_t* X,
+                                     int64_t ldx, uint8_t* Q, int64_t ldq, float* S, int64_t lds, void* stream) {
+    return quantize<uint16_t>(op, block_rows, rows, cols, X, ldx, Q, ldq, S, lds, stream);
+}
+
+gemm_status_t gemm_fp8_quantize_f32(int op, int block_rows, int64_t rows, int64_t cols, const float* X, int64_t ldx,
+                                    uint8_t* Q, int64_t ldq, float* S, int64_t lds, void* stream) {
+    return quantize<float>(op, block_rows, rows, cols, X, ldx, Q, ldq, S, lds, stream);
+}
+
+gemm_status_t gemm_fp8(int64_t M, int64_t N, int64_t K, float alpha, const uint8_t* A, int64_t lda, const float* SA,
+                       int64_t ldsa, const uint8_t* B, int64_t ldb, const float* SB, int64_t ldsb, int b_block_rows,
+                       float beta, uint16_t* C, int64_t ldc, const uint16_t* bias, int act, void* stream) {
+    if (!size_ok(M) || !size_ok(N) || !size_ok(K)) return GEMM_ERR_INVALID_VALUE;
+    if (b_block_rows != 1 && b_block_rows != dg::kScaleBlock) return GEMM_ERR_INVALID_VALUE;
+    const int64_t nk = ceil_div(K, dg::kScaleBlock), nb = ceil_div(N, b_block_rows);
+    if (lda < max1(K) || ldb < max1(K) || ldc < max1(N) || ldsa < max1(M) || ldsb < max1(nb))
+        return GEMM_ERR_INVALID_VALUE;
+    if (!span_ok(2, M, N, ldc) || !span_ok(1, M, K, lda) || !span_ok(1, N, K, ldb) || !span_ok(4, nk, M, ldsa) ||
+        !span_ok(4, nk, nb, ldsb))
+        return GEMM_ERR_INVALID_VALUE;
+    if (!aligned(SA, 4) || !aligned(SB, 4) || !aligned(C, 2) || !valid_epilogue(2, bias, act))
+        return GEMM_ERR_INVALID_VALUE;
+    const Work w = work_of(M, N, K, alpha, beta, bias);
+    if (w == Work::kNone) return GEMM_OK;
+    if (C == nullptr) return GEMM_ERR_INVALID_VALUE;
+    if (w == Work::kGemm && (A == nullptr || SA == nullptr || B == nullptr || SB == nullptr))
+        return GEMM_ERR_INVALID_VALUE;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const dg::Fp8Args a{M, N, K, alpha, beta, A, lda, SA, ldsa, B, ldb, SB, ldsb, b_block_rows, C, ldc, bias, act};
+    return on_device([&](int cus) {
+        return w == Work::kScale ? dg::launch_scale_bf16(M, N, beta, C, ldc, bias, act, s) : dg::launch_fp8(a, cus, s);
+    });
+}
+
+gemm_status_t gemm_bf16_grouped(int opb, int64_t groups, int64_t M, int64_t N, int64_t K, float alpha,
+                                const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t strideb,
+                                float beta, uint16_t* C, int64_t ldc, const int32_t* offsets, const float* row_scale,
+                                const uint16_t* bias, int64_t stridebias, int act, void* stream) {
+    const bool tb = opb == GEMM_OP_T;
+    if (!valid_op(opb) || !size_ok(groups) || !size_ok(M) || !size_ok(N) || !size_ok(K)) return GEMM_ERR_INVALID_VALUE;
+    if (lda < max1(K) || ldb < max1(tb ? K : N) || ldc < max1(N)) return GEMM_ERR_INVALID_VALUE;
+    const int64_t br = tb ? N : K, bc = tb ? K : N;
+    if (!span_ok(2, M, K, lda) || !span_ok(2, br, bc, ldb) || !span_ok(2, M, N, ldc)) return GEMM_ERR_INVALID_VALUE;
+    if (groups > 1) {
+        const int64_t one = br > 0 ? (br - 1) * ldb + bc : 0;
+        if (strideb < 0 || !span_ok(2, groups, one, strideb)) return GEMM_ERR_INVALID_VALUE;
+        if (bias != nullptr && (stridebias < 0 || !span_ok(2, groups, N, stridebias))) return GEMM_ERR_INVALID_VALUE;
+    }
+    if (!aligned(A, 2) || !aligned(B, 2) || !aligned(C, 2) || !aligned(offsets, 4) || !aligned(row_scale, 4) ||
+        !valid_epilogue(2, bias, act))
+        return GEMM_ERR_INVALID_VALUE;
+    if (groups == 0) return GEMM_OK;
+    const Work w = work_of(M, N, K, alpha, beta, bias);
+    if (w == Work::kNone) return GEMM_OK;
+    if (C == nullptr || offsets == nullptr) return GEMM_ERR_INVALID_VALUE;
+    if (w == Work::kGemm && (A == nullptr || B == nullptr)) return GEMM_ERR_INVALID_VALUE;
+    dg::GroupedArgs a{};
+    a.groups = (int)groups;
+    a.M = M; a.N = N; a.K = K;
+    a.alpha = alpha; a.beta = beta;
+    a.A = A; a.lda = lda;
+    a.B = B; a.ldb = ldb; a.strideb = strideb;
+    a.C = C; a.ldc = ldc;
+    a.offsets = offsets;
+    a.tb = tb;
+    a.row_scale = row_scale;
+    a.bias = bias; a.stridebias = stridebias;
+    a.act = act;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    // Without a product (K == 0 or alpha == 0) neither A, B nor the row scales are read.
+    if (w == Work::kScale) {
+        a.K = 0;
+        a.row_scale = nullptr;
+    }
+    return on_device([&](int cus) {
+        return w == Work::kScale ? dg::launch_grouped_general(a, s) : dg::launch_grouped(a, cus, s);
+    });
+}
+
+gemm_status_t gemm_bf16_grouped_wgrad(int64_t groups, int64_t M, int64_t N, int64_t K, float alpha, const uint16_t* X,
+                                      int64_t ldx, const uint16_t* dY, int64_t lddy, float beta, uint16_t* dW,
+                                      int64_t lddw, int64_t stridedw, const int32_t* offsets, void* stream) {
+    return grouped_wgrad(false, groups, M, N, K, alpha, X, ldx, dY, lddy, beta, dW, lddw, stridedw, offsets, stream);
+}
+
+gemm_status_t gemm_bf16_grouped_wgrad_f32(int64_t groups, int64_t M, int64_t N, int64_t K, float alpha,
+                                          const uint16_t* X, int64_t ldx, const uint16_t* dY, int64_t lddy, float beta,
+                                          float* dW, int64_t lddw, int64_t stridedw, const int32_t* offsets,
+                                          void* stream) {
+    return grouped_wgrad(true, groups, M, N, K, alpha, X, ldx, dY, lddy, beta, dW, lddw, stridedw, offsets, stream);
+}
+
+}  // extern "C"

@@ -348,6 +348,121 @@ gemm_status_t gemm_bf16_scaled(int opa, int opb, int64_t M, int64_t N, int64_t K
                                const float* col_scale, const uint16_t* bias, int act,
                                void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- 8-bit operands (OCP e4m3) with a scale for each block of 128 -----------
+ *
+ * A matrix X of rows to multiply is held as e4m3 bytes Q and fp32 scales S:
+ * 128 consecutive values of a row (the dimension a product sums over) share a
+ * scale, alone or together with 128 consecutive rows (block_rows 1 or 128):
+ *
+ *     X(i,k) ~ Q[i*ldq + k] * S[(k / 128) * lds + i / block_rows]
+ *
+ * The scales of one block of 128 k are contiguous over the rows, so that they
+ * are read as the product walks k. ldq >= max(1, row length), lds >=
+ * max(1, ceil(rows / block_rows)); the last block of a row, and the last 128
+ * rows, may be partial.
+ *
+ * gemm_fp8_quantize_bf16 / _f32: with op == GEMM_OP_N quantises X (rows x cols,
+ * row-major, ldx >= max(1,cols)) as it lies, with GEMM_OP_T its transpose (Q is
+ * cols x rows: the operand of a product that sums over X's rows, as a weight's
+ * gradient does). For each block, with top its largest magnitude, but at least
+ * 448 * 2^-126,
+ *
+ *     S = top / 448,   Q = 448 x / top rounded to e4m3, to nearest, ties to even
+ *
+ * (e4m3's largest value is 448). For bf16 input Q is the correct rounding of
+ * the exact quotient; for fp32 input the quotient is rounded to fp32 first.
+ * A block that holds an infinity or a NaN gets S = NaN and Q = 0. Bytes of Q
+ * past a row's end are not written. rows == 0 or cols == 0 does nothing.
+ * GEMM_ERR_INVALID_VALUE as for the other calls, and for an op or block_rows
+ * other than those named. */
+gemm_status_t gemm_fp8_quantize_bf16(int op, int block_rows, int64_t rows, int64_t cols,
+                                     const uint16_t* X, int64_t ldx, uint8_t* Q, int64_t ldq,
+                                     float* S, int64_t lds, void* stream);
+gemm_status_t gemm_fp8_quantize_f32(int op, int block_rows, int64_t rows, int64_t cols,
+                                    const float* X, int64_t ldx, uint8_t* Q, int64_t ldq,
+                                    float* S, int64_t lds, void* stream);
+
+/* Product of two such matrices, both held with k along their rows, C in bf16:
+ *
+ *     C(i,j) <- act(alpha * sum_b SA[b*ldsa + i] * SB[b*ldsb + j / b_block_rows] *
+ *                           sum_{k in block b} A[i*lda + k] * B[j*ldb + k] + bias[j])
+ *               + beta * C(i,j)
+ *
+ * A: M x K (block_rows 1), B: N x K (b_block_rows 1 or 128), as quantised above
+ * or from elsewhere (any e4m3 bytes and any fp32 scales; a NaN byte or scale
+ * gives NaN in the rows and columns it takes part in). The forward product of
+ * a layer y = x W^T takes x and W; its gradients take dY and W quantised
+ * transposed (dX), and dY and X quantised transposed (dW), where B too has a
+ * scale for each row.
+ *
+ * A block's products are summed by the matrix cores' 8-bit instruction, which
+ * aligns the products of each 8 consecutive terms to the largest of them and
+ * keeps at least 13 bits below it; blocks are scaled and summed in fp32, and
+ * the result is rounded to bf16 once. alpha, beta, bias, act, streams and
+ * errors as for gemm_bf16_bias_act (K == 0 or alpha == 0 reads neither A, B nor
+ * the scales). Every alignment and leading dimension is taken; the fast kernels
+ * need A, B and their rows aligned to 16 bytes, and C and its rows to 8. */
+gemm_status_t gemm_fp8(int64_t M, int64_t N, int64_t K, float alpha,
+                       const uint8_t* A, int64_t lda, const float* SA, int64_t ldsa,
+                       const uint8_t* B, int64_t ldb, const float* SB, int64_t ldsb,
+                       int b_block_rows, float beta, uint16_t* C, int64_t ldc,
+                       const uint16_t* bias, int act, void* stream);
+
+/* ---- Products grouped by expert ---------------------------------------------
+ *
+ * The rows of A are sorted by expert: rows offsets[e] .. offsets[e+1] - 1
+ * belong to group e, 0 <= e < groups, whose matrix op(B_e) is K x N (B_e starts
+ * strideb elements after B_{e-1}):
+ *
+ *     C(i,j) <- act(alpha * row_scale[i] * sum_k A(i,k) op(B_e)(k,j) + bias_e[j])
+ *               + beta * C(i,j)          for every row i of every group e
+ *
+ * offsets:   device pointer to groups + 1 values, 0 <= offsets[0] <= .. <=
+ *            offsets[groups] <= M, read by the kernels (the host needs to know
+ *            no group's size, and a captured call follows the values at each
+ *            replay). Groups may be empty. Rows of C outside all groups are
+ *            neither read nor written. Offsets that break the rule give
+ *            undefined values in C's rows, but no access outside the operands.
+ * opb:       GEMM_OP_N: B_e is K x N (ldb >= max(1,N)); GEMM_OP_T: B_e is
+ *            stored N x K (ldb >= max(1,K)). The input's gradient dX = dY op(W)^T
+ *            is the same call with the other opb.
+ * strideb:   >= 0 (0: all groups share one matrix; not read when groups is 1).
+ * row_scale: M fp32 values (a router's weight for each row), or NULL for 1.
+ * bias:      group e's N values at bias + e * stridebias (>= 0), or NULL.
+ * M rows of A and C are allocated; lda, ldc, alpha, beta, act, streams and
+ * errors as for gemm_bf16_op. groups == 0, M == 0 or N == 0 does nothing; K == 0
+ * or alpha == 0 reads neither A, B nor row_scale. No workspace is needed, and
+ * any number of these calls may overlap in time. */
+gemm_status_t gemm_bf16_grouped(int opb, int64_t groups, int64_t M, int64_t N, int64_t K, float alpha,
+                                const uint16_t* A, int64_t lda,
+                                const uint16_t* B, int64_t ldb, int64_t strideb,
+                                float beta, uint16_t* C, int64_t ldc, const int32_t* offsets,
+                                const float* row_scale, const uint16_t* bias, int64_t stridebias,
+                                int act, void* stream);
+
+/* The gradient of the groups' matrices: for every group e
+ *
+ *     dW_e(k,j) <- alpha * sum over the group's rows i of X(i,k) dY(i,j) + beta * dW_e(k,j)
+ *
+ * X: M x K (ldx >= max(1,K)), dY: M x N (lddy >= max(1,N)), bf16; dW_e: K x N
+ * (lddw >= max(1,N)), stridedw elements after dW_{e-1} (at least
+ * (K-1) * lddw + N; not read when groups is 1), in bf16 or, with the _f32 form,
+ * in fp32 (a gradient accumulated over several calls with beta == 1 keeps its
+ * small terms there). Sums are fp32. Weights stored N x K: swap X and dY (and N
+ * and K). An empty group's sum is zero: dW_e <- beta * dW_e. offsets as above;
+ * rows outside all groups are not read. The bias's gradient is the same call
+ * with X a column of ones (K == 1). alpha == 0 or M == 0 reads neither X nor
+ * dY (and beta == 1 then does nothing). Summation order is fixed: the same
+ * call gives the same bits. */
+gemm_status_t gemm_bf16_grouped_wgrad(int64_t groups, int64_t M, int64_t N, int64_t K, float alpha,
+                                      const uint16_t* X, int64_t ldx, const uint16_t* dY, int64_t lddy,
+                                      float beta, uint16_t* dW, int64_t lddw, int64_t stridedw,
+                                      const int32_t* offsets, void* stream);
+gemm_status_t gemm_bf16_grouped_wgrad_f32(int64_t groups, int64_t M, int64_t N, int64_t K, float alpha,
+                                          const uint16_t* X, int64_t ldx, const uint16_t* dY, int64_t lddy,
+                                          float beta, float* dW, int64_t lddw, int64_t stridedw,
+                                          const int32_t* offsets, void* stream);
+
 /* Host-only planning (no HIP call): the variant a call with these arguments
  * would run (a gemm_variant_t value; GEMM_VARIANT_AUTO when the call would
  * launch no GEMM kernel), or -1 when the arguments are invalid. `elem_bytes`
