@@ -105,6 +105,4 @@ hipError_t launch_fp8_general(const Fp8Args& a, hipStream_t s) {
                          dim3((unsigned)(tm * tn)), dim3(256), s, a, tm, tn);
 }
 
-hipError_t launch_fp8(const Fp8Args& a, int, hipStream_t s) { return launch_fp8_general(a, s); }
-
 }  // namespace dg
