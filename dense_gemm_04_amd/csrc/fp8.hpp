@@ -45,6 +45,16 @@ __device__ __forceinline__ i32x8 join16(u32x4 lo, u32x4 hi) {
     return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
+// Zeros the bytes at positions >= keep of a 16-byte chunk.
+__device__ __forceinline__ u32x4 mask_bytes(u32x4 v, int keep) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const int b = keep - 4 * w;
+        v[w] &= b >= 4 ? ~0u : (b <= 0 ? 0u : (1u << (8 * b)) - 1u);
+    }
+    return v;
+}
+
 // Columns col .. col + 3 of one row of C: v[] holds alpha times the product.
 // `wide`: C's rows (and base) are 8-byte aligned.
 template <bool EPI>

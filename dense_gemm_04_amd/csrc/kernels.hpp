@@ -133,10 +133,14 @@ hipError_t launch_quantize(const QuantArgs<float>& a, hipStream_t s);
 // to 8, or any alignment (general).
 hipError_t launch_fp8(const Fp8Args& a, int cus, hipStream_t s);
 hipError_t launch_fp8_general(const Fp8Args& a, hipStream_t s);
+hipError_t launch_fp8_few(const Fp8Args& a, hipStream_t s);
 
 // Products grouped by expert and their weight gradients.
 hipError_t launch_grouped(const GroupedArgs& a, int cus, hipStream_t s);
 hipError_t launch_grouped_general(const GroupedArgs& a, hipStream_t s);
+// Groups of few rows (rows only; alignment as for launch_grouped): tiles of 16
+// or 64 rows by 64 columns, K split over the waves of a workgroup.
+hipError_t launch_grouped_few(const GroupedArgs& a, int rows, hipStream_t s);
 
 // Largest M the small-M kernels accept: the vector kernel (16-byte rows)
 // takes up to 128 rows, the element-wise one up to 32.
