@@ -131,6 +131,4 @@ hipError_t launch_grouped_general(const GroupedArgs& a, hipStream_t s) {
     return launch_kernel(fn, dim3((unsigned)grid), dim3(256), s, a, tm, tn);
 }
 
-hipError_t launch_grouped(const GroupedArgs& a, int, hipStream_t s) { return launch_grouped_general(a, s); }
-
 }  // namespace dg

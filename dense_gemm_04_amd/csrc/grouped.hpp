@@ -94,4 +94,35 @@ __device__ __forceinline__ RowTile find_row_tile(const int32_t* offsets, int gro
     return RowTile{-1, 0, 0};
 }
 
+// The row tile and column of this workgroup: tiles of bm rows by tiles_n
+// columns of tiles, spread over the XCDs in contiguous runs and walked in bands
+// of `band` row tiles. lo, hi: the rows of group `lane` (group_range), from
+// which the tile's group is found where there are at most 64; with more the
+// offsets are read again.
+struct RowPlace {
+    RowTile tile;
+    int tn;
+};
+__device__ __forceinline__ RowPlace place_row_tile(const int32_t* offsets, int groups, int M, int bm, int tiles_n,
+                                                   int band, int lo, int hi, int lane) {
+    const int mine = (int)(((unsigned)(hi - lo) + bm - 1) / bm);
+    const int upto = wave_scan(mine, lane);
+    const bool in_lanes = groups <= 64;
+    const int have = in_lanes ? __builtin_amdgcn_readlane(upto, 63) : count_row_tiles(offsets, groups, M, bm, lane);
+    const int64_t all = (int64_t)have * tiles_n;
+    RowPlace w{RowTile{-1, 0, 0}, 0};
+    if ((int64_t)blockIdx.x >= all) return w;
+    int tm;
+    raster_tile(xcd_slot((int)blockIdx.x, (int)(all < gridDim.x ? all : gridDim.x)), have, tiles_n, band, tm, w.tn);
+    if (in_lanes) {
+        w.tile.group = __builtin_ctzll(__ballot(upto > tm));
+        w.tile.end = __builtin_amdgcn_readlane(hi, w.tile.group);
+        w.tile.m0 = __builtin_amdgcn_readlane(lo, w.tile.group) +
+                    (tm - __builtin_amdgcn_readlane(upto - mine, w.tile.group)) * bm;
+    } else {
+        w.tile = find_row_tile(offsets, groups, M, bm, tm, lane);
+    }
+    return w;
+}
+
 }  // namespace dg
