@@ -316,3 +316,73 @@ def test_layer_forward_and_gradients():
         full, top = exact(), float(np.abs(f64(p)).max() * np.abs(f64(q)).max())
         mags = fp8_ref(np.abs(f64(a)), f64(sa), np.abs(f64(b)), f64(sb), per)[0]
         assert np.all(np.abs(f64(c) - full) <= 0.15 * mags + a.shape[1] * top * 2.0 ** -17 + 2.0 ** -7 * np.abs(full))
+
+
+# Many tiles: whole rounds of resident 256 x 256 tiles and a partly full one,
+# with ragged edges in every dimension, whole tiles only, and one round.
+MANY_TILES = [(5000, 4504, 272), (4352, 4096, 256), (2900, 3301, 400), (2048, 4096, 640)]
+
+
+@pytest.mark.parametrize("b_rows", [1, 128])
+@pytest.mark.parametrize("size", MANY_TILES)
+def test_product_of_many_tiles(size, b_rows):
+    M, N, K = size
+    note(f"fp8 {size} b_rows {b_rows}")
+    up = -(-K // 16) * 16
+    cpu, views = operands(M, N, K, b_rows, M + K, lda=up, ldb=up + 16)
+    g = gen(M)
+    c0, bias = torch.randn(M, N, generator=g).to(torch.bfloat16), torch.randn(N, generator=g).to(torch.bfloat16)
+    ref = [f64(t) for t in cpu]
+    for alpha, beta, act, with_bias in ((1.0, 0.0, dg.ACT_NONE, False), (0.5, -1.0, dg.ACT_RELU, True)):
+        c = run_fp8(views, M, N, K, b_rows, alpha, beta, c0.cuda() if beta else None, bias if with_bias else None, act,
+                    ldc=-(-N // 8) * 8)
+        want, d = fp8_ref(*ref, b_rows, alpha, beta, f64(c0), f64(bias) if with_bias else None, act)
+        assert close(c, want, d, -(-K // 128), instruction=INSTRUCTION) <= 1
+
+
+# One case for each kernel and for the ragged forms of its pipeline.
+CHECKED = [(16, 300, 1000, 128), (30, 8192, 400, 1), (200, 1000, 1040, 128), (500, 4096, 300, 1), (1000, 4100, 400, 128),
+           (1500, 1500, 272, 1), (2100, 2050, 1000, 128), (4700, 4300, 272, 128), (4700, 4300, 272, 1)]
+
+
+@pytest.mark.parametrize("check", ["poison", "sync"])
+@pytest.mark.parametrize("case", CHECKED)
+def test_lds_checking_builds_agree(case, check):
+    """The builds that fill retired LDS stages with NaN and that complete every
+    copy before the next read give the normal build's bits."""
+    M, N, K, b_rows = case
+    note(f"fp8 {check} {case}")
+    lib = dg.load_check_build(check)
+    up = -(-K // 16) * 16
+    _, (a, sa, b, sb) = operands(M, N, K, b_rows, 9, lda=up, ldb=up)
+    out = [torch.full((M, N + 4), float("nan"), dtype=torch.bfloat16, device="cuda")[:, :N] for _ in range(2)]
+    for handle, c in zip((dg.load(), lib), out):
+        st = handle.gemm_fp8(M, N, K, 1.0, a.data_ptr(), ld_of(a), sa.data_ptr(), ld_of(sa), b.data_ptr(), ld_of(b),
+                             sb.data_ptr(), ld_of(sb), b_rows, 0.0, c.data_ptr(), c.stride(0), None, 0, None)
+        torch.cuda.synchronize()
+        assert st == dg.GEMM_OK
+    assert torch.equal(out[0], out[1])
+
+
+def test_conveniences_refuse():
+    q = torch.zeros(64, 256, dtype=torch.uint8, device="cuda")
+    s, s2 = torch.ones(2, 64, device="cuda"), torch.ones(2, 1, device="cuda")
+    c = torch.zeros(64, 64, dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros(64, 256, dtype=torch.bfloat16, device="cuda")
+    dg.matmul_fp8(q, s, q, s2, c)
+    dg.quantize_fp8(x, q, s)
+    for bad in (lambda: dg.matmul_fp8(q, s[:, :63], q, s2, c), lambda: dg.matmul_fp8(q, s, q[:, :200], s2, c),
+                lambda: dg.matmul_fp8(q, s, q, s, c), lambda: dg.matmul_fp8(q, s, q, s2, c[:, :32]),
+                lambda: dg.matmul_fp8(q.t(), s, q, s2, c), lambda: dg.matmul_fp8(q[:1].expand(64, 256), s, q, s2, c),
+                lambda: dg.quantize_fp8(x, q, s[:1]), lambda: dg.quantize_fp8(x, q, s, dg.OP_T),
+                lambda: dg.matmul_fp8(q, s, q, s2, c, bias=c[0, :3])):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: dg.matmul_fp8(x, s, q, s2, c), lambda: dg.matmul_fp8(q, s.double(), q, s2, c),
+                lambda: dg.matmul_fp8(q, s, q, s2, c.float()), lambda: dg.quantize_fp8(x.half(), q, s)):
+        with pytest.raises(TypeError):
+            bad()
+    with pytest.raises(dg.GemmError):
+        dg.matmul_fp8(q, s, q, torch.ones(2, 32, device="cuda"), c, b_block_rows=2)
+    with pytest.raises(dg.GemmError):
+        dg.matmul_fp8(q, s, q, s2, c, act=9)

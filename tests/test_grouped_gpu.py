@@ -313,3 +313,136 @@ def test_captured_calls_follow_the_offsets(lengths):
             assert torch.equal(t, u)
         for o in both:
             assert all(torch.equal(t, u) for t, u in zip(o, want))
+
+
+# Sizes that fill the GPU with 256 x 256 tiles: several rounds, ragged rows,
+# columns and depth; the last with columns that fill no whole vector.
+MANY_TILES = [([2500, 0, 1300, 37, 2163], 4096, 1032), ([4000, 2000], 4104, 1000), ([3000, 1999], 5003, 904)]
+
+
+@pytest.mark.parametrize("tb", [False, True])
+@pytest.mark.parametrize("lengths,N,K", MANY_TILES)
+def test_grouped_many_tiles(lengths, N, K, tb):
+    note(f"grouped many tiles {lengths} {N} {K} tb {tb}")
+    g = gen(N)
+    M, E = sum(lengths) + 7, len(lengths)
+    A, B = normal(g, M, K), normal(g, E, *((N, K) if tb else (K, N)))
+    C0, off, bias = normal(g, M, N), offsets_of(lengths, 3), normal(g, E, N)
+    scale = torch.rand(M, generator=g) + 0.5
+    c = run_grouped(A, B, tb, off, C0, True)
+    want, d = grouped_ref(f64(A), f64(B), tb, off, f64(C0))
+    assert close(c, want, d, K) <= 1
+    c = run_grouped(A, B, tb, off, C0, True, 1.0, 0.5, scale, bias, dg.ACT_RELU)
+    s = f64(scale)[:, None]
+    rows = slice(3, 3 + sum(lengths))
+    group = np.repeat(np.arange(E), lengths)
+    z = want[rows] * s[rows] + f64(bias)[group]
+    full, mags = np.array(f64(C0)), np.zeros_like(d)
+    full[rows] = np.maximum(z, 0) + 0.5 * f64(C0)[rows]
+    mags[rows] = d[rows] * s[rows] + np.abs(f64(bias)[group]) + 0.5 * np.abs(f64(C0)[rows])
+    assert close(c, full, mags, K) <= 1
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lengths,N,K", [([300, 0, 63, 1, 129, 107], 2304, 2304), ([700, 0, 1400], 2051, 2100)])
+def test_wgrad_many_tiles(lengths, N, K, dtype):
+    note(f"wgrad many tiles {lengths} {N} {K} {dtype}")
+    g = gen(K)
+    M, off = sum(lengths) + 5, offsets_of(lengths, 2)
+    X, dY = normal(g, M, K), normal(g, M, N)
+    want, d = wgrad_ref(f64(X), f64(dY), off)
+    step = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
+    dw = run_wgrad(X, dY, off, dtype)
+    assert close(dw, want, d, max(lengths), step) <= 1
+    dW0 = torch.randn(len(lengths), K, N, generator=g).to(dtype)
+    dw = run_wgrad(X, dY, off, dtype, True, 1.0, 1.0, dW0)
+    w0 = f64(dW0)
+    assert close(dw, want + w0, d + np.abs(w0), max(lengths) + 1, step) <= 1
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_more_groups_than_lanes(many):
+    """130 groups, with few rows each and with enough for the tiled kernels."""
+    rng = np.random.default_rng(8)
+    lengths = [int(v) for v in (rng.integers(0, 90, 130) if many else rng.integers(0, 4, 130))]
+    g = gen(70)
+    M, E, N, K = sum(lengths), 130, 200, 136
+    A, B, off, C0 = normal(g, M, K), normal(g, E, K, N), offsets_of(lengths), normal(g, M, N)
+    c = run_grouped(A, B, False, off, C0)
+    want, d = grouped_ref(f64(A), f64(B), False, off, f64(C0))
+    assert close(c, want, d, K) <= 1
+    dY = normal(g, M, N)
+    dw = run_wgrad(A, dY, off, torch.float32)
+    want, d = wgrad_ref(f64(A), f64(dY), off)
+    assert close(dw, want, d, max(lengths), 2.0 ** -24) <= 1
+
+
+@pytest.mark.parametrize("lengths", [[0, 6000, 0, 0], [2000, 2000, 2000], [1, 1, 6000, 1], [700] * 9])
+def test_skewed_and_equal_groups(lengths):
+    """Orders of groups by length: one that holds all rows, equal ones (ties),
+    and single rows beside a long one."""
+    g = gen(71)
+    M, E, N, K = sum(lengths), len(lengths), 264, 200
+    A, dY, off = normal(g, M, K), normal(g, M, N), offsets_of(lengths)
+    dw = run_wgrad(A, dY, off, torch.float32)
+    want, d = wgrad_ref(f64(A), f64(dY), off)
+    assert close(dw, want, d, max(lengths), 2.0 ** -24) <= 1
+    B, C0 = normal(g, E, K, N), normal(g, M, N)
+    c = run_grouped(A, B, False, off, C0)
+    want, d = grouped_ref(f64(A), f64(B), False, off, f64(C0))
+    assert close(c, want, d, K) <= 1
+
+
+CHECKED = [([3, 0, 1, 4], 520, 1000), ([20, 33, 0, 11], 520, 328), ([700, 0, 300, 9], 776, 520), ([64, 130, 200, 0], 300, 264),
+           ([2500, 0, 1300, 2163], 4096, 200)]
+
+
+@pytest.mark.parametrize("check", ["poison", "sync"])
+@pytest.mark.parametrize("lengths,N,K", CHECKED)
+def test_lds_checking_builds_agree(lengths, N, K, check):
+    note(f"grouped {check} {lengths} {N} {K}")
+    g = gen(80)
+    M, E = sum(lengths), len(lengths)
+    x, dy = normal(g, M, K).cuda(), normal(g, M, N).cuda()
+    offs = torch.from_numpy(offsets_of(lengths)).cuda()
+    out = []
+    for handle in (dg.load(), dg.load_check_build(check)):
+        for tb in (False, True):
+            w = normal(gen(81), E, *((N, K) if tb else (K, N))).cuda()
+            y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+            assert handle.gemm_bf16_grouped(int(tb), E, M, N, K, 1.0, x.data_ptr(), K, w.data_ptr(), w.stride(1), w.stride(0),
+                                            0.0, y.data_ptr(), N, offs.data_ptr(), None, None, 0, 0, None) == dg.GEMM_OK
+            torch.cuda.synchronize()
+            out.append(y)
+        for dtype, fn in ((torch.float32, handle.gemm_bf16_grouped_wgrad_f32), (torch.bfloat16, handle.gemm_bf16_grouped_wgrad)):
+            dw = torch.full((E, K, N), float("nan"), dtype=dtype, device="cuda")
+            assert fn(E, M, N, K, 1.0, x.data_ptr(), K, dy.data_ptr(), N, 0.0, dw.data_ptr(), N, K * N, offs.data_ptr(),
+                      None) == dg.GEMM_OK
+            torch.cuda.synchronize()
+            out.append(dw)
+    for a, b in zip(out[:4], out[4:]):
+        assert torch.equal(a, b)
+
+
+def test_conveniences_refuse():
+    x = torch.zeros(64, 32, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(4, 32, 48, dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros(64, 48, dtype=torch.bfloat16, device="cuda")
+    o = torch.zeros(5, dtype=torch.int32, device="cuda")
+    dg.matmul_bf16_grouped(x, w, y, o)
+    dg.grouped_wgrad(x, y, w, o)
+    for bad in (lambda: dg.matmul_bf16_grouped(x, w, y, o[:4]), lambda: dg.matmul_bf16_grouped(x, w, y, o, opb=dg.OP_T),
+                lambda: dg.matmul_bf16_grouped(x[:, :31], w, y, o), lambda: dg.matmul_bf16_grouped(x, w, y[:63], o),
+                lambda: dg.matmul_bf16_grouped(x, w.transpose(1, 2), y, o),
+                lambda: dg.matmul_bf16_grouped(x, w, y, o, row_scale=torch.ones(63, device="cuda")),
+                lambda: dg.matmul_bf16_grouped(x, w, y, o, bias=y[:3]), lambda: dg.grouped_wgrad(x, y[:63], w, o),
+                lambda: dg.grouped_wgrad(x[:1].expand(64, 32), y, w, o), lambda: dg.grouped_wgrad(x, y, w[:, :31], o)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: dg.matmul_bf16_grouped(x, w, y, o.long()), lambda: dg.matmul_bf16_grouped(x.float(), w, y, o),
+                lambda: dg.grouped_wgrad(x, y, w.half(), o)):
+        with pytest.raises(TypeError):
+            bad()
+    # One gradient matrix for all groups: they would overwrite each other.
+    with pytest.raises(dg.GemmError):
+        dg.grouped_wgrad(x, y, w[:1].expand(4, -1, -1), o)
