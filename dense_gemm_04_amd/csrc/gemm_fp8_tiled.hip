@@ -23,6 +23,8 @@
 //     memory at their use they cost every slab 0.3 us: 4096^3 71 against 61 us.)
 //   * B is the instruction's first operand, so a lane holds 4 consecutive
 //     columns of one row of C, and one scale of A serves all of them;
+//   * where 64 x 64 tiles have a CU each, two groups of 4 waves share a tile's K
+//     (KS), so that one's MFMAs run in the other's waits;
 //   * 256 x 256 tiles run one resident workgroup per CU that walks its tiles:
 //     the ring runs on over them, so a tile's first slab lands while the one
 //     before is stored;
@@ -43,8 +45,11 @@ __device__ __forceinline__ int chunk_off(int row, int c) { return row * 128 + ((
 
 // B1: B has a scale for each row (128 rows share one otherwise). The grid may
 // be smaller than the number of tiles: workgroup w takes tiles w, w + grid, ..
-template <int BM, int BN, int WAVES_M, int WAVES_N, int NS, bool EPI, bool B1>
-__global__ __launch_bounds__(WAVES_M * WAVES_N * 64, BM == 256 ? 2 : 4)
+// KS = 2: two groups of waves in one workgroup share a tile, group q over the
+// slabs q, q + 2, .. with a ring of its own; group 1 hands its sums to group 0
+// through LDS (one tile per workgroup). Both groups take every barrier.
+template <int BM, int BN, int WAVES_M, int WAVES_N, int NS, int KS, bool EPI, bool B1>
+__global__ __launch_bounds__(KS * WAVES_M * WAVES_N * 64, BM == 256 ? 2 : 4)
 void gemm_fp8_tiled_kernel(Fp8Args p, int tiles_m, int tiles_n) {
     constexpr int kWaves = WAVES_M * WAVES_N, kNT = kWaves * 64;
     constexpr int kWTM = BM / WAVES_M, kWTN = BN / WAVES_N;
@@ -61,14 +66,18 @@ void gemm_fp8_tiled_kernel(Fp8Args p, int tiles_m, int tiles_n) {
     // A ring of NS stages, [A | B | scales] each.
     constexpr int kAB = BM * 128, kBB = BN * 128, kSB = (kAScl + kBScl) * 256;
     constexpr int kStage = kAB + kBB + kSB;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[NS * kStage];
+    __shared__ __attribute__((aligned(16))) uint8_t all[KS * NS * kStage];
 
     const int64_t M = p.M, N = p.N, K = p.K, lda = p.lda, ldb = p.ldb;
     const int nk = (int)((K + kScaleBlock - 1) / kScaleBlock);
     const int kr = (int)(K - (int64_t)(nk - 1) * kScaleBlock);
     const int tiles = tiles_m * tiles_n, grid = (int)gridDim.x;
-    const int t = threadIdx.x, lane = t & 63;
+    // t and wave count within the group.
+    const int grp = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x / kNT);
+    const int t = (int)threadIdx.x - grp * kNT, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    uint8_t* const lds = all + grp * (NS * kStage);
+    const int turns = (nk + KS - 1) / KS;          // slabs of each group (one past the end where nk is odd)
     const int wm0 = (wave / WAVES_N) * kWTM, wn0 = (wave % WAVES_N) * kWTN;
     const int pl = lane & 15, g = lane >> 4;
 
@@ -92,7 +101,7 @@ void gemm_fp8_tiled_kernel(Fp8Args p, int tiles_m, int tiles_n) {
     const bool scl_a = scl_slot < kAScl;
     const uint32_t scl_chunk = (uint32_t)(scl_a ? scl_slot : scl_slot - kAScl) * 256;
     const int64_t scl_ld = scl_a ? p.ldsa : p.ldsb;
-    int c_id = (int)blockIdx.x, c_kt = 0;
+    int c_id = (int)blockIdx.x, c_kt = grp;
     rsrc_t a_desc, b_desc;
     const float* scl_base;
     uint32_t scl_bytes;
@@ -114,10 +123,11 @@ void gemm_fp8_tiled_kernel(Fp8Args p, int tiles_m, int tiles_n) {
     // and put zeros into a stage that nothing reads any more. With 128 rows to
     // a scale the tile's one or two scales of B lie at the start of their copy.
     auto copy = [&](int q, int st) __attribute__((always_inline)) {
-        const uint32_t k0 = (uint32_t)c_kt * 128u;
+        const bool in = KS == 1 || c_kt < nk;
+        const uint32_t k0 = in ? (uint32_t)c_kt * 128u : 0x80000000u;
         const uint32_t As = lds_addr(lds) + (uint32_t)(st * kStage), Bs = As + kAB, Ss = Bs + kBB;
         if (q == 0) {
-            dma4(make_rsrc(scl_base + c_kt * scl_ld, scl_bytes), (uint32_t)(lane * 4), scl_chunk,
+            dma4(make_rsrc(scl_base + (in ? c_kt : 0) * scl_ld, in ? scl_bytes : 0u), (uint32_t)(lane * 4), scl_chunk,
                  Ss + (scl_a ? 0 : BM * 4) + scl_chunk);
         } else if (q <= kACopies) {
             const int I = wave * kACopies + q - 1;
@@ -128,7 +138,8 @@ void gemm_fp8_tiled_kernel(Fp8Args p, int tiles_m, int tiles_n) {
         }
     };
     auto advance = [&]() __attribute__((always_inline)) {
-        if (++c_kt == nk) {
+        c_kt += KS;
+        if (KS == 1 && c_kt == nk) {
             c_kt = 0;
             c_id += grid;
             aim(c_id);
@@ -252,7 +263,7 @@ void gemm_fp8_tiled_kernel(Fp8Args p, int tiles_m, int tiles_n) {
         }
         // The stage is a number, not a copy of the code for each: copies let
         // the compiler move a slab's additions past the branch between them.
-        for (int kt = 0; kt < nk; ++kt) {
+        for (int turn = 0; turn < turns; ++turn) {
             // This slab has landed (NS - 2 later ones may be on their way), and
             // every read of the slab before, whose stage the cursor's slab
             // takes, is done.
@@ -263,8 +274,8 @@ void gemm_fp8_tiled_kernel(Fp8Args p, int tiles_m, int tiles_n) {
             const int before = st == 0 ? NS - 1 : st - 1;
             if (kLdsCheck == 1) lds_retire(lds + before * kStage, kStage, t, kNT);
             advance();
-            if (kt + 1 == nk && kr < kScaleBlock) {
-                zero_tail(st);
+            if (turn + 1 == turns && kr < kScaleBlock) {
+                if (KS == 1 || turn * KS + grp == nk - 1) zero_tail(st);
                 lds_only_barrier();
             }
             if constexpr (kLdsCheck == 2) copy_all(before);
@@ -277,8 +288,30 @@ void gemm_fp8_tiled_kernel(Fp8Args p, int tiles_m, int tiles_n) {
             for (int j = 0; j < kFN; ++j) add(j, kFM - 1);
         }
 
+        if constexpr (KS == 2) {
+            // Group 1's sums to group 0 through the rings, which both have read
+            // to the end and whose last copies (zeros) have landed: value c of
+            // lane l of wave w at (c waves + w) 64 + l. First half + second half,
+            // the same bits on every call.
+            static_assert(kFM * kFN * kNT * 16 <= KS * NS * kStage, "sums fit");
+            f32x4* const hand = reinterpret_cast<f32x4*>(all) + wave * 64 + lane;
+            lds_barrier();
+            if (grp == 1) {
+#pragma unroll
+                for (int j = 0; j < kFN; ++j)
+#pragma unroll
+                    for (int i = 0; i < kFM; ++i) hand[(j * kFM + i) * kNT] = acc[j][i];
+            }
+            lds_only_barrier();
+            if (grp == 1) return;
+#pragma unroll
+            for (int j = 0; j < kFN; ++j)
+#pragma unroll
+                for (int i = 0; i < kFM; ++i) acc[j][i] += hand[(j * kFM + i) * kNT];
+        }
+
         // ---- epilogue ----
-        if constexpr (kWTN == 64) {
+        if constexpr (kWTN == 64 && KS == 1) {
             if (m0 + BM <= M && n0 + BN <= N) {
                 // Whole tiles: each 16-row block of a wave's results goes
                 // through LDS into row order, so that a lane stores 8 columns
@@ -324,9 +357,10 @@ void gemm_fp8_tiled_kernel(Fp8Args p, int tiles_m, int tiles_n) {
                             for (int e = 0; e < 8; ++e)
                                 v[e] += p.beta * bf16_to_f32((uint16_t)(c0[h][e >> 1] >> (16 * (e & 1))));
                         }
-                        *reinterpret_cast<u32x4_a4*>(crow + 8 * h * p.ldc) =
-                            u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                  pack_bf16x2(v[6], v[7])};
+                        // C would push operands out of L2: 8192 x 12288 x 4096 364 -> 354 us.
+                        const u32x4_a4 out = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                   pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+                        __builtin_nontemporal_store(out, reinterpret_cast<u32x4_a4*>(crow + 8 * h * p.ldc));
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -349,17 +383,16 @@ void gemm_fp8_tiled_kernel(Fp8Args p, int tiles_m, int tiles_n) {
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
 }
 
-template <int BM, int BN, int WAVES_M, int WAVES_N, int NS>
+template <int BM, int BN, int WAVES_M, int WAVES_N, int NS, int KS>
 hipError_t launch_tiles(const Fp8Args& a, int64_t most, hipStream_t s) {
     const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
     if (tm * tn > kMaxGrid) return hipErrorInvalidConfiguration;
     const bool epi = a.bias != nullptr || a.act != kActNone, b1 = a.b_rows == 1;
-    auto fn = epi ? (b1 ? &gemm_fp8_tiled_kernel<BM, BN, WAVES_M, WAVES_N, NS, true, true>
-                        : &gemm_fp8_tiled_kernel<BM, BN, WAVES_M, WAVES_N, NS, true, false>)
-                  : (b1 ? &gemm_fp8_tiled_kernel<BM, BN, WAVES_M, WAVES_N, NS, false, true>
-                        : &gemm_fp8_tiled_kernel<BM, BN, WAVES_M, WAVES_N, NS, false, false>);
+#define DG_F(...) &gemm_fp8_tiled_kernel<BM, BN, WAVES_M, WAVES_N, NS, KS, __VA_ARGS__>
+    auto fn = epi ? (b1 ? DG_F(true, true) : DG_F(true, false)) : (b1 ? DG_F(false, true) : DG_F(false, false));
+#undef DG_F
     const int64_t grid = most > 0 && tm * tn > most ? most : tm * tn;
-    return launch_kernel(fn, dim3((unsigned)grid), dim3(WAVES_M * WAVES_N * 64), s, a, tm, tn);
+    return launch_kernel(fn, dim3((unsigned)grid), dim3(KS * WAVES_M * WAVES_N * 64), s, a, tm, tn);
 }
 
 // Time of a product's tiles in us per slab of K, at 256 CUs: whole rounds of
@@ -380,8 +413,10 @@ double rounds(int64_t M, int64_t N, int bm, int bn, int per_round, double round,
 // 700 x 2048^2: 11.1, 10.1, 12.6, 29.5; 1500^3: 14.7, 14.4, 11.6, 26.5;
 // 2048 x 2560 x 4096: 41.4, 38.1, 40.8, 51.1; 3500 x 3700 x 2000: 65, 56, 54, 34.6.
 // A tile size's time per slab with one, two or a CU's fill of workgroups:
-// 64 x 64 0.36, 0.66, 0.9 (three); 64 x 128 0.5, 0.8; 128 x 128 0.72, 1.3 (two of
-// two stages); 256 x 256 1.75.
+// 64 x 64 0.28, 0.66, 0.9 (three); 64 x 128 0.5, 0.8; 128 x 128 0.72, 1.3 (two of
+// two stages); 256 x 256 1.75. One 64 x 64 tile to a CU runs as two groups of 4
+// waves that share its K (128 x 8192^2 23.3 -> 18.3 us, 1024^2 x 4096 13.5 -> 10.9;
+// two to a CU 509 x 4096 x 4000 23.4 -> 24.5, and at 64 x 128 and 128 x 128 no gain).
 hipError_t launch_fp8(const Fp8Args& a, int cus, hipStream_t s) {
     auto at16 = [](const void* q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld % 16 == 0; };
     const bool rows16 = at16(a.A, a.lda) && at16(a.B, a.ldb);
@@ -390,18 +425,19 @@ hipError_t launch_fp8(const Fp8Args& a, int cus, hipStream_t s) {
     const bool fits = 256 * a.lda + a.K < lim && 256 * a.ldb + a.K < lim;
     if (!rows16 || !c8 || !fits) return launch_fp8_general(a, s);
     if (a.M <= 16 || (a.M <= 32 && a.N <= 8192)) return launch_fp8_few(a, s);
-    const double c64 = rounds(a.M, a.N, 64, 64, 768, 0.9, 0.36, 0.66);
+    const double c64 = rounds(a.M, a.N, 64, 64, 768, 0.9, 0.28, 0.66);
     const double c64w = rounds(a.M, a.N, 64, 128, 512, 0.8, 0.5, 0.8);
     const double c128 = rounds(a.M, a.N, 128, 128, 512, 1.3, 0.72, 1.3);
     const double c256 = rounds(a.M, a.N, 256, 256, 256, 1.75, 1.75, 1.75);
-    if (c256 <= c128 && c256 <= c64w && c256 <= c64) return launch_tiles<256, 256, 2, 4, 2>(a, cus, s);
+    if (c256 <= c128 && c256 <= c64w && c256 <= c64) return launch_tiles<256, 256, 2, 4, 2, 1>(a, cus, s);
     if (c128 <= c64w && c128 <= c64) {
         const int64_t t128 = ((a.M + 127) / 128) * ((a.N + 127) / 128);
-        if (t128 <= 256) return launch_tiles<128, 128, 2, 4, 3>(a, 0, s);
-        return launch_tiles<128, 128, 2, 4, 2>(a, 0, s);
+        if (t128 <= 256) return launch_tiles<128, 128, 2, 4, 3, 1>(a, 0, s);
+        return launch_tiles<128, 128, 2, 4, 2, 1>(a, 0, s);
     }
-    if (c64w <= c64) return launch_tiles<64, 128, 2, 4, 3>(a, 0, s);
-    return launch_tiles<64, 64, 2, 4, 3>(a, 0, s);
+    if (c64w <= c64) return launch_tiles<64, 128, 2, 4, 3, 1>(a, 0, s);
+    if (((a.M + 63) / 64) * ((a.N + 63) / 64) <= 256) return launch_tiles<64, 64, 2, 2, 3, 2>(a, 0, s);
+    return launch_tiles<64, 64, 2, 4, 3, 1>(a, 0, s);
 }
 
 }  // namespace dg

@@ -38,6 +38,10 @@ namespace {
 
 using namespace bf16lds;
 constexpr int kGroupM = 4;
+// Row tiles of one group walked together (place_row_tile). Bands across the
+// groups' ends read two experts' columns side by side: 16 x 16384 x 4096^2 took 577
+// us with bands of 4 over all groups, and within groups 550 (up to 4), 538 (6), 536.
+constexpr int kBand = 8;
 
 template <int BM, int BN, int WAVES_M, int WAVES_N, bool WGRAD, bool TB, bool EPI, bool F32>
 __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, BM == 256 ? 2 : 4)
@@ -100,7 +104,7 @@ void gemm_grouped_kernel(GroupedArgs p, int tiles_m, int tiles_n) {
         B = p.B + l * ldb + n0;
         C = static_cast<CT*>(p.C) + e * p.stridec + m0 * p.ldc;
     } else {
-        const RowPlace w = place_row_tile(p.offsets, p.groups, (int)p.M, BM, tiles_n, kGroupM, lo, hi, lane);
+        const RowPlace w = place_row_tile(p.offsets, p.groups, (int)p.M, BM, tiles_n, kBand, lo, hi, lane);
         if (w.tile.group < 0) return;
         e = w.tile.group;
         const int m0 = w.tile.m0, end = w.tile.end, tn = w.tn;
@@ -281,50 +285,44 @@ void gemm_grouped_kernel(GroupedArgs p, int tiles_m, int tiles_n) {
         const rsrc_t cd = make_rsrc(C + n0, (uint32_t)(((in - 1) * p.ldc + N - n0) * (int64_t)sizeof(CT)));
         constexpr uint32_t kNowhere = 0x80000000u;
         const int left = N - n0 < BN ? (int)(N - n0) : BN;
-        if constexpr (F32) {
+        // Each 16-row block of a wave's results goes through a scratch of its own
+        // in LDS into row order, so that a lane reads and writes 16 bytes of a
+        // row next to its neighbours' (fp32 gradients, 32 x 4096 x 2048^2: 145 us in
+        // the accumulators' order, 130 in row order), not to be kept in the
+        // caches (nt), where C would push operands out (130 -> 109 us).
+        constexpr int kScrLd = kWTN == 64 ? 64 : kWTN + 4, kScrPerStage = kWaves / 2;
+        static_assert(kScrPerStage * 16 * kScrLd * 4 <= kAStage * 2, "half the scratches per A stage");
+        auto scr_at = [](int r, int q) { return r * kScrLd + 4 * (kWTN == 64 ? (q ^ (r & 15)) : q); };
+        constexpr int kNt = 2;                 // cache-policy bit nt
+        constexpr int kLpr = kWTN / kVec, kRpp = 64 / kLpr, kPasses = 16 / kRpp;
+        static_assert(kPasses >= 1, "wave tile");
+        const int cc = lane % kLpr, rr = lane / kLpr, col = wn0 + kVec * cc;
+        const uint32_t lane_off = col < left ? (uint32_t)(col * (int)sizeof(CT)) : kNowhere;
+        float bv[kVec];
+        if constexpr (EPI) {
 #pragma unroll
-            for (int i = 0; i < kFM; ++i) {
-                const uint32_t row = (uint32_t)(wm0 + 16 * i + pl) * ldc;
+            for (int q = 0; q < kVec; ++q)
+                bv[q] = bias != nullptr && col < left ? bf16_to_f32(bias[n0 + col + q]) : 0.f;
+        }
+        lds_only_barrier();                    // every wave has read its last fragments
+        float* scr = reinterpret_cast<float*>(wave < kScrPerStage ? a_st0 : a_st1) +
+                     (wave % kScrPerStage) * 16 * kScrLd;
 #pragma unroll
-                for (int j = 0; j < kFN; ++j) {
-                    const int col = wn0 + 16 * j + 4 * g;
-                    const uint32_t off = col < left ? row + (uint32_t)(4 * col) : kNowhere;
-                    f32x4 v = alpha * acc[j][i];
+        for (int i = 0; i < kFM; ++i) {
+#pragma unroll
+            for (int j = 0; j < kFN; ++j)
+                *reinterpret_cast<f32x4*>(scr + scr_at(pl, 4 * j + g)) = acc[j][i];
+#pragma unroll
+            for (int h = 0; h < kPasses; ++h) {
+                const int r = rr + kRpp * h;
+                const uint32_t off = lane_off + (uint32_t)(wm0 + 16 * i + r) * ldc;
+                if constexpr (F32) {
+                    f32x4 v = alpha * *reinterpret_cast<const f32x4*>(scr + scr_at(r, cc));
                     if (beta != 0.f) v += beta * __builtin_bit_cast(f32x4, buf_load16(cd, off, 0));
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), cd, off, 0, 0);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        } else {
-            // Each 16-row block of a wave's results goes through a scratch of
-            // its own in LDS into row order, so that a lane reads and writes 8
-            // columns of a row.
-            constexpr int kLpr = kWTN / 8, kRpp = 64 / kLpr, kPasses = 16 / kRpp;
-            constexpr int kScrLd = kWTN == 64 ? 64 : kWTN + 4, kScrPerStage = kWaves / 2;
-            static_assert(kPasses >= 1 && kScrPerStage * 16 * kScrLd * 4 <= kAStage * 2, "half the scratches per A stage");
-            auto scr_at = [](int r, int q) { return r * kScrLd + 4 * (kWTN == 64 ? (q ^ (r & 15)) : q); };
-            const int cc = lane % kLpr, rr = lane / kLpr, col = wn0 + 8 * cc;
-            const uint32_t lane_off = col < left ? (uint32_t)(2 * col) : kNowhere;
-            float bv[8];
-            if constexpr (EPI) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    bv[q] = bias != nullptr && col < left ? bf16_to_f32(bias[n0 + col + q]) : 0.f;
-            }
-            lds_only_barrier();                    // every wave has read its last fragments
-            float* scr = reinterpret_cast<float*>(wave < kScrPerStage ? a_st0 : a_st1) +
-                         (wave % kScrPerStage) * 16 * kScrLd;
-#pragma unroll
-            for (int i = 0; i < kFM; ++i) {
-#pragma unroll
-                for (int j = 0; j < kFN; ++j)
-                    *reinterpret_cast<f32x4*>(scr + scr_at(pl, 4 * j + g)) = acc[j][i];
-#pragma unroll
-                for (int h = 0; h < kPasses; ++h) {
-                    const int r = rr + kRpp * h;
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), cd, off, 0, kNt);
+                } else {
                     const f32x4 x = *reinterpret_cast<const f32x4*>(scr + scr_at(r, 2 * cc));
                     const f32x4 y = *reinterpret_cast<const f32x4*>(scr + scr_at(r, 2 * cc + 1));
-                    const uint32_t off = lane_off + (uint32_t)(wm0 + 16 * i + r) * ldc;
                     const float fr = EPI ? factor(wm0 + 16 * i + r) : alpha;
                     float v[8];
 #pragma unroll
@@ -340,10 +338,10 @@ void gemm_grouped_kernel(GroupedArgs p, int tiles_m, int tiles_n) {
                     }
                     __builtin_amdgcn_raw_buffer_store_b128(
                         u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                              pack_bf16x2(v[6], v[7])}, cd, off, 0, 0);
+                              pack_bf16x2(v[6], v[7])}, cd, off, 0, kNt);
                 }
-                __builtin_amdgcn_sched_barrier(0);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
         return;
     }
@@ -399,10 +397,10 @@ double rounds_us(double tiles, double slabs, int per_round, double full, double 
 // not know the groups' sizes: with M rows in E groups it counts on M / bm + E / 2
 // row tiles (a last one for each group, half full), at least one for each group
 // that can have rows. Measured on one MI355X (us; 256, 128 and 64 rows and
-// columns to a tile). Rows, E x M x N x K: 16 x 16384 x 4096^2 578, 683, 1075;
+// columns to a tile). Rows, E x M x N x K: 16 x 16384 x 4096^2 532, 683, 1075;
 // 8 x 8001 x 4096 x 2048 161, 173, 247; 8 x 4096 x 1024 x 2048 46.6, 28.7, 40.6;
 // 32 x 1024 x 4096 x 2048 127, 132, 124; 8 x 16 x 1024 x 4096 83, 41, 34.
-// Gradients: 16 x 16384 x 2048 x 4096 331, 407, 615; 8 x 999 x 1024^2 15.6, 10.2,
+// Gradients: 16 x 16384 x 2048 x 4096 306, 407, 615; 8 x 999 x 1024^2 15.6, 10.2,
 // 12.6; 8 x 8192 x 512^2 50, 27, 20; 2 x 16384 x 2048^2 224, 154, 239.
 int pick_tile(const GroupedArgs& a) {
     const double E = (double)a.groups, M = (double)a.M;

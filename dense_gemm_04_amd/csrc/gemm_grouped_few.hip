@@ -36,9 +36,7 @@ __global__ __launch_bounds__(kW * 64) void gemm_grouped_few_kernel(GroupedArgs p
     const int pl = lane & 15, g = lane >> 4;
     int lo = 0, hi = 0;
     if (lane < p.groups) group_range(p.offsets, lane, (int)p.M, lo, hi);
-    // Bands of one row tile: neighbouring workgroups read neighbouring columns
-    // of one expert's matrix.
-    const RowPlace w = place_row_tile(p.offsets, p.groups, (int)p.M, kRows, tiles_n, 1, lo, hi, lane);
+    const RowPlace w = place_row_tile(p.offsets, p.groups, (int)p.M, kRows, tiles_n, 8, lo, hi, lane);
     if (w.tile.group < 0) return;
     const int e = w.tile.group, m0 = w.tile.m0;
     const int64_t n0 = (int64_t)w.tn * kN, N = p.N, K = p.K, lda = p.lda, ldb = p.ldb;

@@ -95,10 +95,12 @@ __device__ __forceinline__ RowTile find_row_tile(const int32_t* offsets, int gro
 }
 
 // The row tile and column of this workgroup: tiles of bm rows by tiles_n
-// columns of tiles, spread over the XCDs in contiguous runs and walked in bands
-// of `band` row tiles. lo, hi: the rows of group `lane` (group_range), from
-// which the tile's group is found where there are at most 64; with more the
-// offsets are read again.
+// columns of tiles, spread over the XCDs in contiguous runs. A group's tiles lie
+// together and are walked column by column in bands of up to `band` of its row
+// tiles, so that neighbours share their expert's columns and their rows. lo, hi: the
+// rows of group `lane` (group_range), from which the tile's group is found where
+// there are at most 64; with more the offsets are read again and the bands
+// run over the groups' ends.
 struct RowPlace {
     RowTile tile;
     int tn;
@@ -112,14 +114,18 @@ __device__ __forceinline__ RowPlace place_row_tile(const int32_t* offsets, int g
     const int64_t all = (int64_t)have * tiles_n;
     RowPlace w{RowTile{-1, 0, 0}, 0};
     if ((int64_t)blockIdx.x >= all) return w;
+    const int id = xcd_slot((int)blockIdx.x, (int)(all < gridDim.x ? all : gridDim.x));
     int tm;
-    raster_tile(xcd_slot((int)blockIdx.x, (int)(all < gridDim.x ? all : gridDim.x)), have, tiles_n, band, tm, w.tn);
     if (in_lanes) {
-        w.tile.group = __builtin_ctzll(__ballot(upto > tm));
-        w.tile.end = __builtin_amdgcn_readlane(hi, w.tile.group);
-        w.tile.m0 = __builtin_amdgcn_readlane(lo, w.tile.group) +
-                    (tm - __builtin_amdgcn_readlane(upto - mine, w.tile.group)) * bm;
+        const int e = __builtin_ctzll(__ballot((int64_t)upto * tiles_n > id));
+        const int of = __builtin_amdgcn_readlane(mine, e), first = __builtin_amdgcn_readlane(upto, e) - of;
+        const int bands = (of + band - 1) / band;
+        raster_tile(id - first * tiles_n, of, tiles_n, (of + bands - 1) / bands, tm, w.tn);
+        w.tile.group = e;
+        w.tile.end = __builtin_amdgcn_readlane(hi, e);
+        w.tile.m0 = __builtin_amdgcn_readlane(lo, e) + tm * bm;
     } else {
+        raster_tile(id, have, tiles_n, band, tm, w.tn);
         w.tile = find_row_tile(offsets, groups, M, bm, tm, lane);
     }
     return w;
