@@ -11,6 +11,7 @@
 #include "gemm.h"
 #include "common.hpp"
 #include "kernels.hpp"
+#include "ops.hpp"
 
 namespace {
 

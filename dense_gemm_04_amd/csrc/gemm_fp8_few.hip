@@ -10,7 +10,7 @@
 // keeps 16 KB or more on the way.
 
 #include "fp8.hpp"
-#include "kernels.hpp"
+#include "ops.hpp"
 
 namespace dg {
 namespace {

@@ -11,7 +11,7 @@
 
 #include "bf16_lds.hpp"
 #include "fp8.hpp"
-#include "kernels.hpp"
+#include "ops.hpp"
 
 namespace dg {
 namespace {

@@ -34,7 +34,7 @@
 // Operand layout of the MFMA: see mfma_fp8.
 
 #include "fp8.hpp"
-#include "kernels.hpp"
+#include "ops.hpp"
 
 namespace dg {
 namespace {
@@ -61,7 +61,7 @@ void gemm_fp8_tiled_kernel(Fp8Args p, int tiles_m, int tiles_n) {
     static_assert(kACopies * kWaves * 1024 == BM * 128 && kBCopies * kWaves * 1024 == BN * 128, "slabs split evenly");
     // Copies issued after each row of MFMAs: with two stages early in the slab,
     // as they have to land within it (4096^2 x 8192: all after the first row
-    // 115.2 us, over 5 rows 114.1, over all 8 120).
+    // 115.2 us, over 5 rows 114.1, over all 8 118.9).
     constexpr int kPerRow = (NS == 2 ? 2 : 1) * ((kPerSlab + kFM - 1) / kFM);
     // A ring of NS stages, [A | B | scales] each.
     constexpr int kAB = BM * 128, kBB = BN * 128, kSB = (kAScl + kBScl) * 256;

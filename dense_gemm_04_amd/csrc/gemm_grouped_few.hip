@@ -14,7 +14,7 @@
 // (gemm_grouped.hip).
 
 #include "bf16_lds.hpp"
-#include "kernels.hpp"
+#include "ops.hpp"
 
 namespace dg {
 namespace {

@@ -14,7 +14,7 @@
 #include <type_traits>
 
 #include "bf16_lds.hpp"
-#include "kernels.hpp"
+#include "ops.hpp"
 
 namespace dg {
 namespace {

@@ -4,27 +4,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <tuple>
-#include <utility>
-
 #include "common.hpp"
-#include "fp8.hpp"
-#include "grouped.hpp"
 
 namespace dg {
-
-// Launches a kernel with its arguments converted to its parameter types, and
-// returns that launch's own status (not an error left by an earlier call).
-template <typename... P, typename... A>
-hipError_t launch_kernel(void (*fn)(P...), dim3 grid, dim3 block, hipStream_t s, A... args) {
-    std::tuple<P...> vals(static_cast<P>(args)...);
-    return std::apply(
-        [&](auto&... v) {
-            void* kargs[] = {static_cast<void*>(&v)...};
-            return hipLaunchKernel(reinterpret_cast<const void*>(fn), grid, block, kargs, 0, s);
-        },
-        vals);
-}
 
 // Every launcher runs the epilogue instantiation of its kernel when the
 // arguments carry a bias or an activation (has_epilogue).
@@ -114,33 +96,6 @@ hipError_t launch_scale_f32(int64_t M, int64_t N, float beta, float* C, int64_t 
                             const float* bias, int act, hipStream_t s);
 hipError_t launch_scale_bf16(int64_t M, int64_t N, float beta, uint16_t* C, int64_t ldc,
                              const uint16_t* bias, int act, hipStream_t s);
-
-// Quantisation to e4m3 (quantize_fp8.hip): Q is rows x cols, or with
-// `transpose` cols x rows; blocks of 128 along Q's rows by block_rows of them.
-template <typename T>
-struct QuantArgs {
-    bool transpose;
-    int block_rows;                 // 1 or 128
-    int64_t rows, cols;             // of X
-    const T* X; int64_t ldx;
-    uint8_t* Q; int64_t ldq;
-    float* S; int64_t lds;
-};
-hipError_t launch_quantize(const QuantArgs<uint16_t>& a, hipStream_t s);
-hipError_t launch_quantize(const QuantArgs<float>& a, hipStream_t s);
-
-// The 8-bit block-scaled product: rows of A and B aligned to 16 bytes and of C
-// to 8, or any alignment (general).
-hipError_t launch_fp8(const Fp8Args& a, int cus, hipStream_t s);
-hipError_t launch_fp8_general(const Fp8Args& a, hipStream_t s);
-hipError_t launch_fp8_few(const Fp8Args& a, hipStream_t s);
-
-// Products grouped by expert and their weight gradients.
-hipError_t launch_grouped(const GroupedArgs& a, int cus, hipStream_t s);
-hipError_t launch_grouped_general(const GroupedArgs& a, hipStream_t s);
-// Groups of few rows (rows only; alignment as for launch_grouped): tiles of 16
-// or 64 rows by 64 columns, K split over the waves of a workgroup.
-hipError_t launch_grouped_few(const GroupedArgs& a, int rows, hipStream_t s);
 
 // Largest M the small-M kernels accept: the vector kernel (16-byte rows)
 // takes up to 128 rows, the element-wise one up to 32.

@@ -20,7 +20,7 @@
 // of the copy.
 
 #include "fp8.hpp"
-#include "kernels.hpp"
+#include "ops.hpp"
 
 namespace dg {
 namespace {
