@@ -511,6 +511,9 @@ namespace {
 
 bool size_ok(int64_t x) { return x >= 0 && x <= INT_MAX; }
 
+// The kernels walk the groups 64 at a time with an int.
+bool groups_ok(int64_t x) { return x >= 0 && x <= INT_MAX - 64; }
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Status of the launch on the current device.
@@ -544,7 +547,7 @@ gemm_status_t grouped_wgrad(bool f32, int64_t groups, int64_t M, int64_t N, int6
                             int64_t ldx, const uint16_t* dY, int64_t lddy, float beta, void* dW, int64_t lddw,
                             int64_t stridedw, const int32_t* offsets, void* stream) {
     const int esz = f32 ? 4 : 2;
-    if (!size_ok(groups) || !size_ok(M) || !size_ok(N) || !size_ok(K)) return GEMM_ERR_INVALID_VALUE;
+    if (!groups_ok(groups) || !size_ok(M) || !size_ok(N) || !size_ok(K)) return GEMM_ERR_INVALID_VALUE;
     if (ldx < max1(K) || lddy < max1(N) || lddw < max1(N)) return GEMM_ERR_INVALID_VALUE;
     if (!span_ok(2, M, K, ldx) || !span_ok(2, M, N, lddy) || !span_ok(esz, K, N, lddw)) return GEMM_ERR_INVALID_VALUE;
     const int64_t one = K > 0 ? (K - 1) * lddw + N : 0;
@@ -559,7 +562,7 @@ gemm_status_t grouped_wgrad(bool f32, int64_t groups, int64_t M, int64_t N, int6
     a.wgrad = true;
     a.groups = (int)groups;
     a.M = product ? M : 0; a.N = N; a.K = K;
-    a.alpha = alpha; a.beta = beta;
+    a.alpha = product ? alpha : 0.f; a.beta = beta;
     a.A = X; a.lda = ldx;
     a.B = dY; a.ldb = lddy;
     a.C = dW; a.ldc = lddw; a.stridec = stridedw;
@@ -612,7 +615,7 @@ gemm_status_t gemm_bf16_grouped(int opb, int64_t groups, int64_t M, int64_t N, i
                                 float beta, uint16_t* C, int64_t ldc, const int32_t* offsets, const float* row_scale,
                                 const uint16_t* bias, int64_t stridebias, int act, void* stream) {
     const bool tb = opb == GEMM_OP_T;
-    if (!valid_op(opb) || !size_ok(groups) || !size_ok(M) || !size_ok(N) || !size_ok(K)) return GEMM_ERR_INVALID_VALUE;
+    if (!valid_op(opb) || !groups_ok(groups) || !size_ok(M) || !size_ok(N) || !size_ok(K)) return GEMM_ERR_INVALID_VALUE;
     if (lda < max1(K) || ldb < max1(tb ? K : N) || ldc < max1(N)) return GEMM_ERR_INVALID_VALUE;
     const int64_t br = tb ? N : K, bc = tb ? K : N;
     if (!span_ok(2, M, K, lda) || !span_ok(2, br, bc, ldb) || !span_ok(2, M, N, ldc)) return GEMM_ERR_INVALID_VALUE;
@@ -645,6 +648,7 @@ gemm_status_t gemm_bf16_grouped(int opb, int64_t groups, int64_t M, int64_t N, i
     // Without a product (K == 0 or alpha == 0) neither A, B nor the row scales are read.
     if (w == Work::kScale) {
         a.K = 0;
+        a.alpha = 0.f;
         a.row_scale = nullptr;
     }
     return on_device([&](int cus) {

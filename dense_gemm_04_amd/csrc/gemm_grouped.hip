@@ -262,7 +262,7 @@ void gemm_grouped_kernel(GroupedArgs p, int tiles_m, int tiles_n) {
     }
 
     // ---- epilogue: acc[j][i] register r is C(wm0 + 16 i + pl, n0 + wn0 + 16 j + 4 g + r) ----
-    const float alpha = p.alpha, beta = p.beta;
+    const float alpha = WGRAD && depth == 0 ? 0.f : p.alpha, beta = p.beta;     // an empty sum is 0, also times inf
     const uint16_t* bias = EPI && p.bias != nullptr ? p.bias + e * p.stridebias : nullptr;
     const int64_t in = rows < BM ? rows : BM;
     const bool scaled = EPI && p.row_scale != nullptr;

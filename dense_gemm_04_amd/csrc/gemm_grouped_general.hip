@@ -98,7 +98,8 @@ __global__ __launch_bounds__(256) void gemm_grouped_general_kernel(GroupedArgs p
     for (int i = 0; i < 2; ++i) {
         const int64_t row = wm + 16 * i + pl;
         if (row >= rows) continue;
-        const float fr = row_scale != nullptr ? p.alpha * row_scale[row] : p.alpha;
+        const float alpha = WGRAD && depth == 0 ? 0.f : p.alpha;       // an empty sum is 0, also times inf
+        const float fr = row_scale != nullptr ? alpha * row_scale[row] : alpha;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll

@@ -431,8 +431,10 @@ gemm_status_t gemm_fp8(int64_t M, int64_t N, int64_t K, float alpha,
  * bias:      group e's N values at bias + e * stridebias (>= 0), or NULL.
  * M rows of A and C are allocated; lda, ldc, alpha, beta, act, streams and
  * errors as for gemm_bf16_op. groups == 0, M == 0 or N == 0 does nothing; K == 0
- * or alpha == 0 reads neither A, B nor row_scale. No workspace is needed, and
- * any number of these calls may overlap in time. */
+ * or alpha == 0 reads neither A, B nor row_scale. Every alignment is taken; the
+ * fast kernels need A, B, C, their rows and strideb aligned to 16 bytes. No
+ * workspace is needed, and any number of these calls may overlap in time. At
+ * most 2^31 - 65 groups. */
 gemm_status_t gemm_bf16_grouped(int opb, int64_t groups, int64_t M, int64_t N, int64_t K, float alpha,
                                 const uint16_t* A, int64_t lda,
                                 const uint16_t* B, int64_t ldb, int64_t strideb,

@@ -129,3 +129,9 @@ def test_the_tests_own_rounding():
     np.testing.assert_array_equal(nearest_e4m3(v.float().double().numpy()), want)
     _, s = quantize_ref(np.array([[0.0, 448.0]]), 1)
     assert s[0, 0] == 1.0
+
+
+def test_group_counts_past_the_kernels_counters_are_refused():
+    for groups in ((1 << 31) - 64, (1 << 31) - 1):
+        assert grouped(groups=groups, strideb=0) == BAD
+        assert wgrad(groups=groups) == BAD
