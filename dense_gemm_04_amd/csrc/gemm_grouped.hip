@@ -271,97 +271,87 @@ void gemm_grouped_kernel(GroupedArgs p, int tiles_m, int tiles_n) {
         if (!scaled) return alpha;
         return alpha * __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(scale_desc, 4 * row, 0, 0));
     };
-    // Lanes hold whole vectors of columns: C through a descriptor of the tile's
-    // rows, past which nothing is loaded or stored; lanes past the last column
-    // address past its end too. The stores' whole offset is the lane's: with
-    // part of it in the scalar offset the compiler sees no hazard between a
-    // 128-bit store and an instruction right after it that writes the store's
-    // last data register, and on this GPU there is one (fp32 gradients of
-    // one-row groups held, now and then, the next vector's last column in 4 of
-    // 16 lanes).
+    // C through a descriptor of the tile's rows, past which nothing is loaded or
+    // stored (its end on a whole dword, as loads are cut by dwords); lanes past
+    // the last column address past its end too, and the lane whose vector
+    // crosses the last column stores its elements one by one (gradients,
+    // 17 x 8824 x 3434 x 1408 in fp32: 168 us, against 272 with every lane's
+    // elements stored one by one in the accumulators' order). The stores' whole
+    // offset is the lane's: with part of it in the scalar offset the compiler
+    // sees no hazard between a 128-bit store and an instruction right after it
+    // that writes the store's last data register, and on this GPU there is one
+    // (fp32 gradients of one-row groups held, now and then, the next vector's
+    // last column in 4 of 16 lanes).
     constexpr int kVec = F32 ? 4 : 8;
-    if (N % kVec == 0) {
-        const uint32_t ldc = (uint32_t)(p.ldc * (int64_t)sizeof(CT));
-        const rsrc_t cd = make_rsrc(C + n0, (uint32_t)(((in - 1) * p.ldc + N - n0) * (int64_t)sizeof(CT)));
-        constexpr uint32_t kNowhere = 0x80000000u;
-        const int left = N - n0 < BN ? (int)(N - n0) : BN;
-        // Each 16-row block of a wave's results goes through a scratch of its own
-        // in LDS into row order, so that a lane reads and writes 16 bytes of a
-        // row next to its neighbours' (fp32 gradients, 32 x 4096 x 2048^2: 145 us in
-        // the accumulators' order, 130 in row order), not to be kept in the
-        // caches (nt), where C would push operands out (130 -> 109 us).
-        constexpr int kScrLd = kWTN == 64 ? 64 : kWTN + 4, kScrPerStage = kWaves / 2;
-        static_assert(kScrPerStage * 16 * kScrLd * 4 <= kAStage * 2, "half the scratches per A stage");
-        auto scr_at = [](int r, int q) { return r * kScrLd + 4 * (kWTN == 64 ? (q ^ (r & 15)) : q); };
-        constexpr int kNt = 2;                 // cache-policy bit nt
-        constexpr int kLpr = kWTN / kVec, kRpp = 64 / kLpr, kPasses = 16 / kRpp;
-        static_assert(kPasses >= 1, "wave tile");
-        const int cc = lane % kLpr, rr = lane / kLpr, col = wn0 + kVec * cc;
-        const uint32_t lane_off = col < left ? (uint32_t)(col * (int)sizeof(CT)) : kNowhere;
-        float bv[kVec];
-        if constexpr (EPI) {
+    const uint32_t ldc = (uint32_t)(p.ldc * (int64_t)sizeof(CT));
+    const rsrc_t cd = make_rsrc(C + n0, (uint32_t)((((in - 1) * p.ldc + N - n0) * (int64_t)sizeof(CT) + 3) & ~(int64_t)3));
+    constexpr uint32_t kNowhere = 0x80000000u;
+    const int left = N - n0 < BN ? (int)(N - n0) : BN;
+    // Each 16-row block of a wave's results goes through a scratch of its own
+    // in LDS into row order, so that a lane reads and writes 16 bytes of a
+    // row next to its neighbours' (fp32 gradients, 32 x 4096 x 2048^2: 145 us in
+    // the accumulators' order, 130 in row order), not to be kept in the
+    // caches (nt), where C would push operands out (130 -> 109 us).
+    constexpr int kScrLd = kWTN == 64 ? 64 : kWTN + 4, kScrPerStage = kWaves / 2;
+    static_assert(kScrPerStage * 16 * kScrLd * 4 <= kAStage * 2, "half the scratches per A stage");
+    auto scr_at = [](int r, int q) { return r * kScrLd + 4 * (kWTN == 64 ? (q ^ (r & 15)) : q); };
+    constexpr int kNt = 2;                 // cache-policy bit nt
+    constexpr int kLpr = kWTN / kVec, kRpp = 64 / kLpr, kPasses = 16 / kRpp;
+    static_assert(kPasses >= 1, "wave tile");
+    const int cc = lane % kLpr, rr = lane / kLpr, col = wn0 + kVec * cc;
+    const uint32_t lane_off = col < left ? (uint32_t)(col * (int)sizeof(CT)) : kNowhere;
+    const bool ragged = N % kVec != 0, part = col < left && left - col < kVec;
+    // 16 bytes of C at byte `off`, this lane's first column there.
+    auto store = [&](u32x4 v, uint32_t off) __attribute__((always_inline)) {
+        __builtin_amdgcn_raw_buffer_store_b128(v, cd, ragged && part ? kNowhere : off, 0, kNt);
+        if (!ragged || !part) return;
 #pragma unroll
-            for (int q = 0; q < kVec; ++q)
-                bv[q] = bias != nullptr && col < left ? bf16_to_f32(bias[n0 + col + q]) : 0.f;
+        for (int q = 0; q < kVec; ++q) {
+            if (col + q >= left) continue;
+            if constexpr (F32) __builtin_amdgcn_raw_buffer_store_b32(v[q], cd, off + 4 * q, 0, 0);
+            else __builtin_amdgcn_raw_buffer_store_b16((short)(v[q >> 1] >> (16 * (q & 1))), cd, off + 2 * q, 0, 0);
         }
-        lds_only_barrier();                    // every wave has read its last fragments
-        float* scr = reinterpret_cast<float*>(wave < kScrPerStage ? a_st0 : a_st1) +
-                     (wave % kScrPerStage) * 16 * kScrLd;
+    };
+    float bv[kVec];
+    if constexpr (EPI) {
 #pragma unroll
-        for (int i = 0; i < kFM; ++i) {
-#pragma unroll
-            for (int j = 0; j < kFN; ++j)
-                *reinterpret_cast<f32x4*>(scr + scr_at(pl, 4 * j + g)) = acc[j][i];
-#pragma unroll
-            for (int h = 0; h < kPasses; ++h) {
-                const int r = rr + kRpp * h;
-                const uint32_t off = lane_off + (uint32_t)(wm0 + 16 * i + r) * ldc;
-                if constexpr (F32) {
-                    f32x4 v = alpha * *reinterpret_cast<const f32x4*>(scr + scr_at(r, cc));
-                    if (beta != 0.f) v += beta * __builtin_bit_cast(f32x4, buf_load16(cd, off, 0));
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), cd, off, 0, kNt);
-                } else {
-                    const f32x4 x = *reinterpret_cast<const f32x4*>(scr + scr_at(r, 2 * cc));
-                    const f32x4 y = *reinterpret_cast<const f32x4*>(scr + scr_at(r, 2 * cc + 1));
-                    const float fr = EPI ? factor(wm0 + 16 * i + r) : alpha;
-                    float v[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        v[q] = fr * (q < 4 ? x[q] : y[q - 4]);
-                        if constexpr (EPI) v[q] = activate(v[q] + bv[q], p.act);
-                    }
-                    if (beta != 0.f) {
-                        const u32x4 c0 = buf_load16(cd, off, 0);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            v[q] += beta * bf16_to_f32((uint16_t)(c0[q >> 1] >> (16 * (q & 1))));
-                    }
-                    __builtin_amdgcn_raw_buffer_store_b128(
-                        u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                              pack_bf16x2(v[6], v[7])}, cd, off, 0, kNt);
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        return;
+        for (int q = 0; q < kVec; ++q)
+            bv[q] = bias != nullptr && col + q < left ? bf16_to_f32(bias[n0 + col + q]) : 0.f;
     }
+    lds_only_barrier();                    // every wave has read its last fragments
+    float* scr = reinterpret_cast<float*>(wave < kScrPerStage ? a_st0 : a_st1) +
+                 (wave % kScrPerStage) * 16 * kScrLd;
 #pragma unroll
     for (int i = 0; i < kFM; ++i) {
-        const int64_t row = wm0 + 16 * i + pl;
-        if (row >= in) continue;
-        CT* crow = C + row * p.ldc;
-        const float fr = EPI ? factor((int)row) : alpha;
 #pragma unroll
-        for (int j = 0; j < kFN; ++j) {
+        for (int j = 0; j < kFN; ++j)
+            *reinterpret_cast<f32x4*>(scr + scr_at(pl, 4 * j + g)) = acc[j][i];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int64_t col = n0 + wn0 + 16 * j + 4 * g + r;
-                if (col >= N) continue;
-                float v = fr * acc[j][i][r];
-                if constexpr (EPI) v = activate(v + (bias != nullptr ? bf16_to_f32(bias[col]) : 0.f), p.act);
-                if (beta != 0.f) v += beta * elem_f32(crow[col]);
-                if constexpr (F32) crow[col] = v;
-                else crow[col] = f32_to_bf16(v);
+        for (int h = 0; h < kPasses; ++h) {
+            const int r = rr + kRpp * h;
+            const uint32_t off = lane_off + (uint32_t)(wm0 + 16 * i + r) * ldc;
+            if constexpr (F32) {
+                f32x4 v = alpha * *reinterpret_cast<const f32x4*>(scr + scr_at(r, cc));
+                if (beta != 0.f) v += beta * __builtin_bit_cast(f32x4, buf_load16(cd, off, 0));
+                store(__builtin_bit_cast(u32x4, v), off);
+            } else {
+                const f32x4 x = *reinterpret_cast<const f32x4*>(scr + scr_at(r, 2 * cc));
+                const f32x4 y = *reinterpret_cast<const f32x4*>(scr + scr_at(r, 2 * cc + 1));
+                const float fr = EPI ? factor(wm0 + 16 * i + r) : alpha;
+                float v[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    v[q] = fr * (q < 4 ? x[q] : y[q - 4]);
+                    if constexpr (EPI) v[q] = activate(v[q] + bv[q], p.act);
+                }
+                if (beta != 0.f) {
+                    const u32x4 c0 = buf_load16(cd, off, 0);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        v[q] += beta * bf16_to_f32((uint16_t)(c0[q >> 1] >> (16 * (q & 1))));
+                }
+                store(u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                            pack_bf16x2(v[6], v[7])}, off);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
