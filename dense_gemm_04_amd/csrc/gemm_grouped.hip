@@ -391,7 +391,11 @@ double rounds_us(double tiles, double slabs, int per_round, double full, double 
 // 8 x 8001 x 4096 x 2048 161, 173, 247; 8 x 4096 x 1024 x 2048 46.6, 28.7, 40.6;
 // 32 x 1024 x 4096 x 2048 127, 132, 124; 8 x 16 x 1024 x 4096 83, 41, 34.
 // Gradients: 16 x 16384 x 2048 x 4096 306, 407, 615; 8 x 999 x 1024^2 15.6, 10.2,
-// 12.6; 8 x 8192 x 512^2 50, 27, 20; 2 x 16384 x 2048^2 224, 154, 239.
+// 12.6; 8 x 8192 x 512^2 50, 27, 20; 2 x 16384 x 2048^2 224, 154, 239. 0 is the
+// few-row kernel on tiles of 64 rows (rows only), one workgroup to a CU whose
+// waves share K: with few tiles, 64 x 64 here and there: 4 x 400 x 1024 x 4096 34.2
+// and 16.6, 2 x 1749 x 256 x 1536 15.2 and 9.2, 3 x 600 x 1024 x 3264 (B stored N x K)
+// 27.4 and 13.2, 8 x 256 x 2048^2 20.4 and 16.8; 6 x 812 x 2560 x 1544 22.7 and 27.9.
 int pick_tile(const GroupedArgs& a) {
     const double E = (double)a.groups, M = (double)a.M;
     auto edges = [](int64_t n, int b) { return (double)((n + b - 1) / b); };
@@ -404,6 +408,8 @@ int pick_tile(const GroupedArgs& a) {
     const double t256 = rounds_us(tiles(256), slabs, 256, 1.8, a.wgrad ? 1.8 : 1.3, 1.8, 8);
     const double t128 = rounds_us(tiles(128), slabs, 512, 1.18, 0.65, 1.1, 5);
     const double t64 = rounds_us(tiles(64), slabs, 1024, 1.05, 0.55, a.wgrad ? 0.6 : 1.05, 3);
+    const double few = a.wgrad ? 1e30 : rounds_us(tiles(64), slabs, 256, 0.32, 0.24, 0.24, 4);
+    if (few < t256 && few < t128 && few < t64) return 0;
     return t256 <= t128 && t256 <= t64 ? 256 : t128 <= t64 ? 128 : 64;
 }
 
@@ -438,6 +444,7 @@ hipError_t launch_grouped(const GroupedArgs& a, int, hipStream_t s) {
     switch (pick_tile(a)) {
         case 256: return launch_tiles<256, 256, 2, 4>(a, s);
         case 128: return launch_tiles<128, 128, 2, 4>(a, s);
+        case 0: return launch_grouped_few(a, 64, s);
         default: return launch_tiles<64, 64, 2, 2>(a, s);
     }
 }
