@@ -49,6 +49,7 @@ hipError_t launch_fp8_few(const Fp8Args& a, hipStream_t s);
 // Products grouped by expert and their weight gradients.
 hipError_t launch_grouped(const GroupedArgs& a, int cus, hipStream_t s);
 hipError_t launch_grouped_general(const GroupedArgs& a, hipStream_t s);
+hipError_t launch_grouped_192(const GroupedArgs& a, hipStream_t s);    // rows only, called by launch_grouped
 // Groups of few rows (rows only; alignment as for launch_grouped): tiles of 16
 // or 64 rows by 64 columns, K split over the waves of a workgroup.
 hipError_t launch_grouped_few(const GroupedArgs& a, int rows, hipStream_t s);

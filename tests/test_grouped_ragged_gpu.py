@@ -44,3 +44,39 @@ def test_gradients(lengths, N, K, dtype):
     want, d = wgrad_ref(f64(X), f64(dY), off, 0.5, -0.25, f64(dW0))
     step = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
     assert close(dw, want, d, max(lengths) + 1, step) <= 1
+
+
+# Few enough tiles that 192 rows to a tile make one round, 256 rows a worse one.
+@pytest.mark.parametrize("tb", [False, True])
+@pytest.mark.parametrize("N,K", [(4091, 200), (4096, 328), (4093, 72)])
+def test_tiles_of_192_rows(N, K, tb):
+    note(f"grouped 192 {N} {K} {tb}")
+    lengths = [1300, 0, 1250]
+    g, E, M = gen(N + K), len(lengths), sum(lengths) + 3
+    A, B = normal(g, M, K), normal(g, E, *((N, K) if tb else (K, N)))
+    off, C0 = offsets_of(lengths), normal(g, M, N)
+    c = run_grouped(A, B, tb, off, C0)
+    want, d = grouped_ref(f64(A), f64(B), tb, off, f64(C0))
+    assert close(c, want, d, K) <= 1
+    scale, bias = torch.rand(M, generator=g) + 0.5, normal(g, E, N)
+    c = run_grouped(A, B, tb, off, C0, True, 0.5, -0.5, scale, bias, dg.ACT_RELU)
+    want, d = grouped_ref(f64(A), f64(B), tb, off, f64(C0), 0.5, -0.5, f64(scale), f64(bias), dg.ACT_RELU)
+    assert close(c, want, d, K) <= 1
+
+
+@pytest.mark.parametrize("check", ["poison", "sync"])
+def test_tiles_of_192_rows_in_the_lds_checking_builds(check):
+    M, E, N, K, g = 2550, 2, 4096, 264, gen(9)
+    x = normal(g, M, K).cuda()
+    offs = torch.tensor([0, 1300, M], dtype=torch.int32, device="cuda")
+    for tb in (False, True):
+        w = normal(g, E, *((N, K) if tb else (K, N))).cuda()
+        out = []
+        for handle in (dg.load(), dg.load_check_build(check)):
+            y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+            assert handle.gemm_bf16_grouped(int(tb), E, M, N, K, 1.0, x.data_ptr(), K, w.data_ptr(), w.stride(1),
+                                            w.stride(0), 0.0, y.data_ptr(), N, offs.data_ptr(), None, None, 0, 0,
+                                            None) == dg.GEMM_OK
+            torch.cuda.synchronize()
+            out.append(y)
+        assert torch.equal(*out)
