@@ -14,8 +14,8 @@
 // without the multiply-adds it takes 1.6, with copies that read nothing 1.25. So
 // the copies' way through L2 is what is left, then the multiply-adds.
 //
-//   * 8 waves, each 128 x 64 of a 256 x 256 tile (or a smaller share of a
-//     smaller tile); K in slabs of 128 in a ring of NS LDS stages, copied with
+//   * 8 waves, each 128 x 64 of a 256 x 256 tile (96 x 64 of 192 x 256, or a smaller
+//     share of a smaller tile); K in slabs of 128 in a ring of NS LDS stages, copied with
 //     LDS-destined 128-bit loads, A and B in rows of 128 bytes whose 16-byte
 //     chunk c lies at c ^ (row mod 8): the fragment reads meet no bank conflict;
 //   * the slab's scales travel with it: 256-byte copies from SA and SB, whose
@@ -25,7 +25,7 @@
 //     columns of one row of C, and one scale of A serves all of them;
 //   * where 64 x 64 tiles have a CU each, two groups of 4 waves share a tile's K
 //     (KS), so that one's MFMAs run in the other's waits;
-//   * 256 x 256 tiles run one resident workgroup per CU that walks its tiles:
+//   * 256 x 256 and 192 x 256 tiles run one resident workgroup per CU that walks its tiles:
 //     the ring runs on over them, so a tile's first slab lands while the one
 //     before is stored;
 //   * edges: descriptors end where the matrices end (rows past M and N arrive
@@ -49,7 +49,7 @@ __device__ __forceinline__ int chunk_off(int row, int c) { return row * 128 + ((
 // slabs q, q + 2, .. with a ring of its own; group 1 hands its sums to group 0
 // through LDS (one tile per workgroup). Both groups take every barrier.
 template <int BM, int BN, int WAVES_M, int WAVES_N, int NS, int KS, bool EPI, bool B1>
-__global__ __launch_bounds__(KS * WAVES_M * WAVES_N * 64, BM == 256 ? 2 : 4)
+__global__ __launch_bounds__(KS * WAVES_M * WAVES_N * 64, BM >= 192 ? 2 : 4)
 void gemm_fp8_tiled_kernel(Fp8Args p, int tiles_m, int tiles_n) {
     constexpr int kWaves = WAVES_M * WAVES_N, kNT = kWaves * 64;
     constexpr int kWTM = BM / WAVES_M, kWTN = BN / WAVES_N;
@@ -414,9 +414,12 @@ double rounds(int64_t M, int64_t N, int bm, int bn, int per_round, double round,
 // 2048 x 2560 x 4096: 41.4, 38.1, 40.8, 51.1; 3500 x 3700 x 2000: 65, 56, 54, 34.6.
 // A tile size's time per slab with one, two or a CU's fill of workgroups:
 // 64 x 64 0.28, 0.66, 0.9 (three); 64 x 128 0.5, 0.8; 128 x 128 0.72, 1.3 (two of
-// two stages); 256 x 256 1.75. One 64 x 64 tile to a CU runs as two groups of 4
-// waves that share its K (128 x 8192^2 23.3 -> 18.3 us, 1024^2 x 4096 13.5 -> 10.9;
-// two to a CU 509 x 4096 x 4000 23.4 -> 24.5, and at 64 x 128 and 128 x 128 no gain).
+// two stages); 192 x 256 1.4; 256 x 256 1.75. 192 x 256 saves what 256 x 256 leaves
+// empty in a last round (3346 x 6144 x 4912 142 -> 124 us, 6000^2 x 3000 with a scale
+// per row of B 162 -> 135, 5550 x 1478 x 5756 70 -> 60, 4813 x 3710 x 720 38 -> 29).
+// One 64 x 64 tile to a CU runs as two groups of 4 waves that share its K
+// (128 x 8192^2 23.3 -> 18.3 us, 1024^2 x 4096 13.5 -> 10.9; two to a CU 509 x 4096 x
+// 4000 23.4 -> 24.5, and at 64 x 128 and 128 x 128 no gain).
 hipError_t launch_fp8(const Fp8Args& a, int cus, hipStream_t s) {
     auto at16 = [](const void* q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld % 16 == 0; };
     const bool rows16 = at16(a.A, a.lda) && at16(a.B, a.ldb);
@@ -429,6 +432,9 @@ hipError_t launch_fp8(const Fp8Args& a, int cus, hipStream_t s) {
     const double c64w = rounds(a.M, a.N, 64, 128, 512, 0.8, 0.5, 0.8);
     const double c128 = rounds(a.M, a.N, 128, 128, 512, 1.3, 0.72, 1.3);
     const double c256 = rounds(a.M, a.N, 256, 256, 256, 1.75, 1.75, 1.75);
+    const double c192 = rounds(a.M, a.N, 192, 256, 256, 1.4, 1.4, 1.4);
+    if (c192 < c256 && c192 <= c128 && c192 <= c64w && c192 <= c64)
+        return launch_tiles<192, 256, 2, 4, 2, 1>(a, cus, s);
     if (c256 <= c128 && c256 <= c64w && c256 <= c64) return launch_tiles<256, 256, 2, 4, 2, 1>(a, cus, s);
     if (c128 <= c64w && c128 <= c64) {
         const int64_t t128 = ((a.M + 127) / 128) * ((a.N + 127) / 128);
