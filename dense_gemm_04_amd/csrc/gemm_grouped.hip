@@ -63,7 +63,7 @@ double rounds_us(double tiles, double slabs, int per_round, double full, double 
 // not know the groups' sizes: with M rows in E groups it counts on M / bm + E / 2
 // row tiles (a last one for each group, half full), at least one for each group
 // that can have rows. Measured on one MI355X (us; 256, 128 and 64 rows and
-// columns to a tile). Rows, E x M x N x K: 16 x 16384 x 4096^2 532, 683, 1075;
+// columns to a tile). Rows, E x M x N x K: 16 x 16384 x 4096^2 520, 610, 1075;
 // 8 x 8001 x 4096 x 2048 150, 170, 247; 8 x 4096 x 1024 x 2048 46.6, 28.7, 40.6;
 // 32 x 1024 x 4096 x 2048 127, 132, 124; 8 x 16 x 1024 x 4096 83, 41, 34.
 // Gradients: 16 x 16384 x 2048 x 4096 306, 407, 615; 8 x 999 x 1024^2 15.6, 10.2,
