@@ -157,15 +157,19 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // Issued as inline assembly so that the compiler neither reorders LDS
 // accesses across it nor inserts waits for it: the kernel's own vmcnt wait
 // plus barrier (lds_barrier) is the only thing that consumes these copies.
+// A copy may read m0 only one wait state after the scalar unit has written it.
+// The compiler keeps that distance for instructions of its own, not inside
+// inline assembly, so the s_nop is part of the copy; without it a copy could
+// land at the LDS address of the one before.
 __device__ __forceinline__ void dma16(rsrc_t r, uint32_t voff, uint32_t soff, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                  :: "v"(voff), "s"(r), "s"(soff), "s"(lds) : "memory", "m0");
 }
 
 // The same with 4 bytes per lane (buffer_load_dword ... lds): lane l's dword
 // lands at lds + 4 l. Global addresses need only 4-byte alignment.
 __device__ __forceinline__ void dma4(rsrc_t r, uint32_t voff, uint32_t soff, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dword %0, %1, %2 offen lds"
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
                  :: "v"(voff), "s"(r), "s"(soff), "s"(lds) : "memory", "m0");
 }
 
