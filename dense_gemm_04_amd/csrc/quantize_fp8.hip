@@ -12,7 +12,10 @@
 // either side. Each element therefore takes one correction step,
 //     q0 = y r,  q = q0 + (y - q0 t) r   (y = 0.875 x, t = top / 512, r ~ 1/t),
 // whose two fused multiply-adds give the correctly rounded quotient; y is exact
-// for bf16, never overflows, and r stays a normal number for every top.
+// for bf16, never overflows, and r stays a normal number for every top. Where
+// top is below 2^-60, y and t are both taken 2^64 times as large: y - q0 t can
+// be 2^-34 of t where q is small, and has to be held exactly (a residual lost
+// below the smallest fp32 number would leave q on either side of a tie).
 //
 // Bound by memory: one read of X and one write of Q, every value held in
 // registers between the two; 4 fp32 operations, an unpack and half a
@@ -90,7 +93,8 @@ __device__ __forceinline__ uint32_t top8(const Raw8<float>& x) {
 }
 
 struct Block {
-    float t, r, s;     // top / 512, its reciprocal, the scale
+    float t, r, s;     // top / 512 (times 2^64 where top is small), its reciprocal, the scale
+    float f;           // y = f x
     bool bad;          // an infinity or NaN in the block
 };
 
@@ -100,13 +104,15 @@ __device__ __forceinline__ Block block_of(uint32_t bits) {
     float top = __builtin_bit_cast(float, bits);
     top = (b.bad || top < kMinTop) ? kMinTop : top;
     b.s = b.bad ? __builtin_nanf("") : top / kE4m3Max;
-    b.t = top * 0x1p-9f;
+    const bool small = top < 0x1p-60f;
+    b.f = small ? 0.875f * 0x1p64f : 0.875f;
+    b.t = top * (small ? 0x1p55f : 0x1p-9f);
     b.r = 1.f / b.t;
     return b;
 }
 
 __device__ __forceinline__ float quotient(float x, const Block& b) {
-    const float y = 0.875f * x, q0 = y * b.r;
+    const float y = b.f * x, q0 = y * b.r;
     return __builtin_fmaf(__builtin_fmaf(-q0, b.t, y), b.r, q0);
 }
 

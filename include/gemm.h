@@ -370,7 +370,8 @@ gemm_status_t gemm_bf16_scaled(int opa, int opb, int64_t M, int64_t N, int64_t K
  *     S = top / 448,   Q = 448 x / top rounded to e4m3, to nearest, ties to even
  *
  * (e4m3's largest value is 448). For bf16 input Q is the correct rounding of
- * the exact quotient; for fp32 input the quotient is rounded to fp32 first.
+ * the exact quotient; for fp32 input the quotient reaches that rounding with
+ * two fp32 roundings behind it, within 2^-23 of itself.
  * A block that holds an infinity or a NaN gets S = NaN and Q = 0. Bytes of Q
  * past a row's end are not written. rows == 0 or cols == 0 does nothing.
  * GEMM_ERR_INVALID_VALUE as for the other calls, and for an op or block_rows
