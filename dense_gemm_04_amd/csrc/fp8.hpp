@@ -17,6 +17,12 @@ constexpr float kMinTop = 0x1.cp-118f;       // 448 * 2^-126
 
 // C <- act(alpha * sum_b SA(b,i) SB(b, j / b_rows) sum_{k in b} A(i,k) B(j,k)
 //          + bias[j]) + beta * C; SA(b,i) = SA[b * ldsa + i], SB alike.
+// Every kernel forms SA SB in fp32 and adds the block's sum times it in one
+// fused step, so that scales at the ends of fp32's range give the same values
+// whatever kernel the alignment chooses. (Scaling in two steps, or by mantissas
+// and exponents where the product leaves the normal numbers, would hold a wider
+// range: the first doubles the vector work of the tiles, the second's branch
+// spills 42 to 215 registers of the two largest.)
 struct Fp8Args {
     int64_t M, N, K;
     float alpha, beta;

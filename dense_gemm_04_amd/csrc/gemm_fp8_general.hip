@@ -5,8 +5,8 @@
 //
 // One workgroup of 4 waves per 64 x 64 tile, each wave a 32 x 32 quarter; K in
 // blocks of 128, the block that shares a scale: its product (one
-// v_mfma_f32_16x16x128_f8f6f4 per 16 x 16) is scaled in fp32 and added to the
-// accumulator. B is the instruction's first operand, so a lane holds 4
+// v_mfma_f32_16x16x128_f8f6f4 per 16 x 16) is scaled by SA SB, formed first and
+// in fp32 as in the aligned kernels, and added to the accumulator. B is the instruction's first operand, so a lane holds 4
 // consecutive columns of one row of C. Elements past M, N and K are zeros.
 
 #include "bf16_lds.hpp"
@@ -81,7 +81,7 @@ __global__ __launch_bounds__(256) void gemm_fp8_general_kernel(Fp8Args p, int ti
             for (int i = 0; i < 2; ++i) {
                 const f32x4 d = mfma_fp8(fb[j], fa[i]);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[j][i][r] = __builtin_fmaf(d[r] * sa[i], sb[j][r], acc[j][i][r]);
+                for (int r = 0; r < 4; ++r) acc[j][i][r] = __builtin_fmaf(d[r], sa[i] * sb[j][r], acc[j][i][r]);
             }
     }
 #pragma unroll

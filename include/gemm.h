@@ -390,8 +390,14 @@ gemm_status_t gemm_fp8_quantize_f32(int op, int block_rows, int64_t rows, int64_
  *               + beta * C(i,j)
  *
  * A: M x K (block_rows 1), B: N x K (b_block_rows 1 or 128), as quantised above
- * or from elsewhere (any e4m3 bytes and any fp32 scales; a NaN byte or scale
- * gives NaN in the rows and columns it takes part in). The forward product of
+ * or from elsewhere (any e4m3 bytes; a NaN byte or scale gives NaN in the rows
+ * and columns it takes part in). The scales are fp32 values whose product
+ * SA * SB, for every two blocks that meet, is formed in fp32: where it leaves
+ * the normal numbers, the block counts with the product as fp32 holds it
+ * (subnormal or 0 below 2^-126; infinite from 2^128 on, which gives NaN with a
+ * block whose sum is 0). Operands quantised above stay within while the largest
+ * values of two such blocks multiply to 2^-108 .. 2^145, or one block is zeros.
+ * The forward product of
  * a layer y = x W^T takes x and W; its gradients take dY and W quantised
  * transposed (dX), and dY and X quantised transposed (dW), where B too has a
  * scale for each row.
