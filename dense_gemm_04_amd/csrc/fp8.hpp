@@ -40,9 +40,11 @@ struct Fp8Args {
 // row p of `x` and of `y`, and receives D(row 4 g + r of x, row p of y) in
 // register r. Which k a byte position means is free as long as both operands
 // agree. The instruction aligns the products of each 8 k to the largest of
-// them and keeps 13 bits below it (measured on in-range operands), so a block's
-// sum is within 8 * 2^-13 of the largest product of each 8, far below the
-// rounding of C to bf16; everything after it, over blocks, is fp32.
+// them and keeps 13 bits below it (measured on in-range operands): a sum is
+// within 8 * 2^-13 = 2^-10 of the sum of its terms' magnitudes at worst, which
+// can exceed bf16's half step where the terms cancel. Measured over K of
+// 1040 to 4100, normal values: 4.4e-5 to 6.1e-5 of C, root-mean-square, where
+// rounding C to bf16 gives 1.7e-3. Everything after a block, over blocks, is fp32.
 __device__ __forceinline__ f32x4 mfma_fp8(i32x8 x, i32x8 y) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }

@@ -131,7 +131,8 @@ hipError_t launch_cfg(const Fp8Args& a, hipStream_t s) {
 }  // namespace
 
 // M <= 32. Tiles of 16 or 32 columns: the wider ones read A half as often,
-// the narrower ones are twice as many. One MI355X, us with 16 and with 32
+// the narrower ones are twice as many. 32 columns run where they make one round
+// that fills more than half of the 256 CUs (129 to 256 tiles). One MI355X, us with 16 and with 32
 // columns: 16 x 8192^2 18.0 and 14.2, 16 x 4096 x 8192 10.5 and 13.9, 5 x 12288 x
 // 4096 12.3 and 13.5; 32 x 8192^2 27.7 and 17.9, 32 x 4096^2 9.4 and 10.7.
 hipError_t launch_fp8_few(const Fp8Args& a, hipStream_t s) {

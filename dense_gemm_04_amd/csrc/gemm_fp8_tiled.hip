@@ -6,13 +6,18 @@
 // of C, from zero; its fp32 result times SA SB is added to the accumulator by
 // the vector units. The block scales differ along k, so the matrix core cannot
 // accumulate across blocks itself; 4 multiply-adds per lane take half the
-// cycles of the MFMA they follow and run beside the next ones.
+// cycles of the MFMA they follow and run beside the next ones. With a scale for
+// each row of B, SA SB differs by element: a multiply and a multiply-add each,
+// as many cycles as the MFMAs (4096^2 x 8192 131 us, 110 without the multiply;
+// with 128 rows to a scale 113).
 //
 // Bound: at 256 x 256 tiles a slab of 128 k holds 32 MFMAs per wave, 2048 cycles
 // of each matrix core; 64 KB of copies into LDS and 192 KB of fragment reads
 // pass beside them. On one MI355X a slab takes 1.7 us, about half of it MFMA:
 // without the multiply-adds it takes 1.6, with copies that read nothing 1.25. So
-// the copies' way through L2 is what is left, then the multiply-adds.
+// the copies' way through L2 is what is left, then the multiply-adds. Smaller
+// tiles, one or two to a CU, wait for their copies at every slab's barrier:
+// 509 x 4096 x 4000 on 64 x 128 tiles copies 768 KB per CU in 19.6 us, 40 GB/s.
 //
 //   * 8 waves, each 128 x 64 of a 256 x 256 tile (96 x 64 of 192 x 256, or a smaller
 //     share of a smaller tile); K in slabs of 128 in a ring of NS LDS stages, copied with
@@ -411,7 +416,9 @@ double rounds(int64_t M, int64_t N, int bm, int bn, int per_round, double round,
 // kernel, but 32 x 8192^2 22.4 and 17.9; 48 x 8192^2 22.5 and 23.0.
 // 96 x 8192^2: 64 x 64 22.8, 64 x 128 28.4, 128 x 128 36.0, 256 x 256 83;
 // 700 x 2048^2: 11.1, 10.1, 12.6, 29.5; 1500^3: 14.7, 14.4, 11.6, 26.5;
-// 2048 x 2560 x 4096: 41.4, 38.1, 40.8, 51.1; 3500 x 3700 x 2000: 65, 56, 54, 34.6.
+// 2048 x 2560 x 4096: 41.4, 38.1, 40.8, 51.1; 3500 x 3700 x 2000: 65, 56, 54, 34.6;
+// 64 x 64, 64 x 128 and 128 x 128: 509 x 4096 x 4000 23.5, 19.6, 23.9, 512 x 4096 x 8192
+// 32.8, 29.7, 39.5. The model counts 256 CUs, the whole card.
 // A tile size's time per slab with one, two or a CU's fill of workgroups:
 // 64 x 64 0.28, 0.66, 0.9 (three); 64 x 128 0.5, 0.8; 128 x 128 0.72, 1.3 (two of
 // two stages); 192 x 256 1.4; 256 x 256 1.75. 192 x 256 saves what 256 x 256 leaves

@@ -59,7 +59,8 @@ double rounds_us(double tiles, double slabs, int per_round, double full, double 
     return whole * (full * slabs + edge) + (rem < 0.5 ? 0.0 : last * slabs + edge);
 }
 
-// The tile size whose rounds of resident workgroups cost least. The host does
+// The tile size whose rounds of resident workgroups cost least, on 256 CUs (the
+// whole card). The host does
 // not know the groups' sizes: with M rows in E groups it counts on M / bm + E / 2
 // row tiles (a last one for each group, half full), at least one for each group
 // that can have rows. Measured on one MI355X (us; 256, 128 and 64 rows and
@@ -76,6 +77,9 @@ double rounds_us(double tiles, double slabs, int per_round, double full, double 
 // stored N x K 143 and 149, 4 x 12000 x 2816 x 2048 131 and 149, 8 x 5000 x 4096^2 184
 // and 196, 2 x 2500 x 4096 x 2048 40 and 47; 16 x 16384 x 4096^2 522 and 517,
 // 8 x 6000 x 4096 x 1024 66 and 56.
+// A gradient's workgroup sums all of its group's rows, so few small matrices
+// with many rows leave CUs empty: 2 x 16384 x 256^2 takes 74 us on 32 workgroups
+// of 128 slabs, for 17 MB of operands; 2 x 16384 x 512^2 75, 8 x 16384 x 256^2 33.
 int pick_tile(const GroupedArgs& a) {
     const double E = (double)a.groups, M = (double)a.M;
     auto edges = [](int64_t n, int b) { return (double)((n + b - 1) / b); };

@@ -404,11 +404,15 @@ gemm_status_t gemm_fp8_quantize_f32(int op, int block_rows, int64_t rows, int64_
  *
  * A block's products are summed by the matrix cores' 8-bit instruction, which
  * aligns the products of each 8 consecutive terms to the largest of them and
- * keeps at least 13 bits below it; blocks are scaled and summed in fp32, and
- * the result is rounded to bf16 once. alpha, beta, bias, act, streams and
+ * keeps at least 13 bits below it (so a sum is within 2^-10 of the sum of its
+ * terms' magnitudes; about 5e-5 of C, root-mean-square, for normal values);
+ * blocks are scaled and summed in fp32, and the result is rounded to bf16
+ * once. alpha, beta, bias, act, streams and
  * errors as for gemm_bf16_bias_act (K == 0 or alpha == 0 reads neither A, B nor
  * the scales). Every alignment and leading dimension is taken; the fast kernels
- * need A, B and their rows aligned to 16 bytes, and C and its rows to 8. */
+ * need A, B and their rows aligned to 16 bytes, and C and its rows to 8. Other
+ * operands are loaded element by element, 10 to 30 times slower on large
+ * products (2048^3: 236 us against 18.5). */
 gemm_status_t gemm_fp8(int64_t M, int64_t N, int64_t K, float alpha,
                        const uint8_t* A, int64_t lda, const float* SA, int64_t ldsa,
                        const uint8_t* B, int64_t ldb, const float* SB, int64_t ldsb,
@@ -439,7 +443,9 @@ gemm_status_t gemm_fp8(int64_t M, int64_t N, int64_t K, float alpha,
  * M rows of A and C are allocated; lda, ldc, alpha, beta, act, streams and
  * errors as for gemm_bf16_op. groups == 0, M == 0 or N == 0 does nothing; K == 0
  * or alpha == 0 reads neither A, B nor row_scale. Every alignment is taken; the
- * fast kernels need A, B, C, their rows and strideb aligned to 16 bytes. No
+ * fast kernels need A, B, C, their rows and strideb aligned to 16 bytes, and
+ * other operands are loaded element by element, about 12 times slower on large
+ * products (8 groups, 2048 x 2048^2: 342 us against 27). No
  * workspace is needed, and any number of these calls may overlap in time. At
  * most 2^31 - 65 groups. */
 gemm_status_t gemm_bf16_grouped(int opb, int64_t groups, int64_t M, int64_t N, int64_t K, float alpha,
@@ -462,7 +468,9 @@ gemm_status_t gemm_bf16_grouped(int opb, int64_t groups, int64_t M, int64_t N, i
  * rows outside all groups are not read. The bias's gradient is the same call
  * with X a column of ones (K == 1). alpha == 0 or M == 0 reads neither X nor
  * dY (and beta == 1 then does nothing). Summation order is fixed: the same
- * call gives the same bits. */
+ * call gives the same bits. Alignment as above (X, dY, dW, their rows and
+ * stridedw). One workgroup sums a whole group's rows for its tile of dW_e: a few
+ * small matrices with very many rows leave most of the GPU idle. */
 gemm_status_t gemm_bf16_grouped_wgrad(int64_t groups, int64_t M, int64_t N, int64_t K, float alpha,
                                       const uint16_t* X, int64_t ldx, const uint16_t* dY, int64_t lddy,
                                       float beta, uint16_t* dW, int64_t lddw, int64_t stridedw,
