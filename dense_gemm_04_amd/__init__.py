@@ -6,7 +6,8 @@ device pointers (ints), sizes, leading dimensions and a stream handle (int,
 the library is missing or cannot be loaded, every call raises.
 
 ``matmul_f32`` / ``matmul_bf16``, ``quantize_fp8`` / ``matmul_fp8`` and
-``matmul_bf16_grouped`` / ``grouped_wgrad`` are conveniences that take torch CUDA
+``matmul_bf16_grouped`` / ``grouped_wgrad``, and ``layernorm``, ``dropout`` and the
+``moe_*`` calls with their gradients, are conveniences that take torch CUDA
 tensors (row-major, unit column stride), pass their pointers, strides and
 torch's current stream, and raise ``GemmError`` on a non-zero status.
 """
@@ -47,8 +48,17 @@ EXPORTS = ("gemm_f32", "gemm_bf16", "gemm_f32_ex", "gemm_bf16_ex", "gemm_bf16_ws
            "gemm_f32_bias_act", "gemm_bf16_bias_act", "gemm_f32_op", "gemm_bf16_op",
            "gemm_f32_scaled", "gemm_bf16_scaled", "gemm_fp8_quantize_bf16",
            "gemm_fp8_quantize_f32", "gemm_fp8", "gemm_bf16_grouped", "gemm_bf16_grouped_wgrad",
-           "gemm_bf16_grouped_wgrad_f32", "gemm_plan",
+           "gemm_bf16_grouped_wgrad_f32", "gemm_layernorm_bf16", "gemm_layernorm_f32",
+           "gemm_layernorm_grad_workspace_size", "gemm_layernorm_grad_bf16",
+           "gemm_layernorm_grad_f32", "gemm_dropout_bf16", "gemm_dropout_f32",
+           "gemm_moe_route_workspace_size", "gemm_moe_route_bf16", "gemm_moe_route_f32",
+           "gemm_moe_route_grad_bf16", "gemm_moe_route_grad_f32", "gemm_moe_gather_bf16",
+           "gemm_moe_combine_bf16", "gemm_moe_combine_grad_bf16", "gemm_plan",
            "gemm_status_string")
+
+# Limits of the router (experts) and of a token's choices (k).
+MOE_MAX_EXPERTS = 1024
+MOE_MAX_K = 16
 
 _lib = None
 
@@ -119,6 +129,34 @@ def _bind(path: str) -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = ci, [i64, i64, i64, i64, f32, vp, i64, vp, i64, f32, vp, i64, i64,
                                        vp, vp]
+    for name in ("gemm_layernorm_bf16", "gemm_layernorm_f32"):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = ci, [i64, i64, f32, vp, i64, vp, vp, vp, i64, vp, vp, vp]
+    for name in ("gemm_layernorm_grad_bf16", "gemm_layernorm_grad_f32"):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = ci, [i64, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, i64, f32,
+                                       vp, vp, vp, ctypes.c_size_t, vp]
+    for name in ("gemm_dropout_bf16", "gemm_dropout_f32"):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = ci, [i64, i64, f32, vp, vp, i64, vp, i64, vp, i64, vp]
+    for name in ("gemm_moe_route_bf16", "gemm_moe_route_f32"):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = ci, [i64, i64, ci, ci, vp, i64, vp, vp, vp, vp, vp, vp, vp,
+                                       ctypes.c_size_t, vp]
+    for name in ("gemm_moe_route_grad_bf16", "gemm_moe_route_grad_f32"):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = ci, [i64, i64, ci, ci, vp, i64, vp, vp, vp, vp, vp, i64, vp]
+    lib.gemm_layernorm_grad_workspace_size.restype = ctypes.c_size_t
+    lib.gemm_layernorm_grad_workspace_size.argtypes = [i64, i64]
+    lib.gemm_moe_route_workspace_size.restype = ctypes.c_size_t
+    lib.gemm_moe_route_workspace_size.argtypes = [i64, i64, ci]
+    lib.gemm_moe_gather_bf16.restype = ci
+    lib.gemm_moe_gather_bf16.argtypes = [i64, ci, i64, i64, vp, i64, vp, vp, i64, vp]
+    lib.gemm_moe_combine_bf16.restype = ci
+    lib.gemm_moe_combine_bf16.argtypes = [i64, ci, i64, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp]
+    lib.gemm_moe_combine_grad_bf16.restype = ci
+    lib.gemm_moe_combine_grad_bf16.argtypes = [i64, ci, i64, i64, vp, i64, vp, i64, vp, vp, vp, i64,
+                                               vp, vp]
     lib.gemm_plan.restype = ci
     lib.gemm_plan.argtypes = [ci, i64, i64, i64, f32, vp, i64, vp, i64, f32, vp, i64, ci]
     lib.gemm_status_string.restype = ctypes.c_char_p
@@ -236,6 +274,90 @@ def gemm_bf16_grouped_wgrad_f32(groups, M, N, K, alpha, X, ldx, dY, lddy, beta, 
                                 offsets, stream=0) -> int:
     return load().gemm_bf16_grouped_wgrad_f32(groups, M, N, K, alpha, X, ldx, dY, lddy, beta, dW,
                                               lddw, stridedw, offsets, stream)
+
+
+def gemm_layernorm_bf16(rows, cols, eps, X, ldx, weight, bias, Y, ldy, mean=None, rstd=None,
+                        stream=0) -> int:
+    return load().gemm_layernorm_bf16(rows, cols, eps, X, ldx, weight, bias, Y, ldy, mean, rstd,
+                                      stream)
+
+
+def gemm_layernorm_f32(rows, cols, eps, X, ldx, weight, bias, Y, ldy, mean=None, rstd=None,
+                       stream=0) -> int:
+    return load().gemm_layernorm_f32(rows, cols, eps, X, ldx, weight, bias, Y, ldy, mean, rstd,
+                                     stream)
+
+
+def gemm_layernorm_grad_workspace_size(rows, cols) -> int:
+    return load().gemm_layernorm_grad_workspace_size(rows, cols)
+
+
+def gemm_layernorm_grad_bf16(rows, cols, X, ldx, weight, mean, rstd, dY, lddy, R, ldr, dX, lddx,
+                             beta, dweight, dbias, workspace, workspace_bytes, stream=0) -> int:
+    return load().gemm_layernorm_grad_bf16(rows, cols, X, ldx, weight, mean, rstd, dY, lddy, R, ldr,
+                                           dX, lddx, beta, dweight, dbias, workspace,
+                                           workspace_bytes, stream)
+
+
+def gemm_layernorm_grad_f32(rows, cols, X, ldx, weight, mean, rstd, dY, lddy, R, ldr, dX, lddx,
+                            beta, dweight, dbias, workspace, workspace_bytes, stream=0) -> int:
+    return load().gemm_layernorm_grad_f32(rows, cols, X, ldx, weight, mean, rstd, dY, lddy, R, ldr,
+                                          dX, lddx, beta, dweight, dbias, workspace,
+                                          workspace_bytes, stream)
+
+
+def gemm_dropout_bf16(rows, cols, p, rng, X, ldx, R, ldr, Y, ldy, stream=0) -> int:
+    return load().gemm_dropout_bf16(rows, cols, p, rng, X, ldx, R, ldr, Y, ldy, stream)
+
+
+def gemm_dropout_f32(rows, cols, p, rng, X, ldx, R, ldr, Y, ldy, stream=0) -> int:
+    return load().gemm_dropout_f32(rows, cols, p, rng, X, ldx, R, ldr, Y, ldy, stream)
+
+
+def gemm_moe_route_workspace_size(tokens, experts, k) -> int:
+    return load().gemm_moe_route_workspace_size(tokens, experts, k)
+
+
+def gemm_moe_route_bf16(tokens, experts, k, renormalize, logits, ldl, gates, choice, slots, offsets,
+                        counts, loss, workspace, workspace_bytes, stream=0) -> int:
+    return load().gemm_moe_route_bf16(tokens, experts, k, renormalize, logits, ldl, gates, choice,
+                                      slots, offsets, counts, loss, workspace, workspace_bytes,
+                                      stream)
+
+
+def gemm_moe_route_f32(tokens, experts, k, renormalize, logits, ldl, gates, choice, slots, offsets,
+                       counts, loss, workspace, workspace_bytes, stream=0) -> int:
+    return load().gemm_moe_route_f32(tokens, experts, k, renormalize, logits, ldl, gates, choice,
+                                     slots, offsets, counts, loss, workspace, workspace_bytes,
+                                     stream)
+
+
+def gemm_moe_route_grad_bf16(tokens, experts, k, renormalize, logits, ldl, choice, counts, dgates,
+                             dloss, dlogits, lddl, stream=0) -> int:
+    return load().gemm_moe_route_grad_bf16(tokens, experts, k, renormalize, logits, ldl, choice,
+                                           counts, dgates, dloss, dlogits, lddl, stream)
+
+
+def gemm_moe_route_grad_f32(tokens, experts, k, renormalize, logits, ldl, choice, counts, dgates,
+                            dloss, dlogits, lddl, stream=0) -> int:
+    return load().gemm_moe_route_grad_f32(tokens, experts, k, renormalize, logits, ldl, choice,
+                                          counts, dgates, dloss, dlogits, lddl, stream)
+
+
+def gemm_moe_gather_bf16(tokens, k, cols, rows, X, ldx, slots, Y, ldy, stream=0) -> int:
+    return load().gemm_moe_gather_bf16(tokens, k, cols, rows, X, ldx, slots, Y, ldy, stream)
+
+
+def gemm_moe_combine_bf16(tokens, k, cols, rows, Y, ldy, slots, gates, R, ldr, C, ldc,
+                          stream=0) -> int:
+    return load().gemm_moe_combine_bf16(tokens, k, cols, rows, Y, ldy, slots, gates, R, ldr, C, ldc,
+                                        stream)
+
+
+def gemm_moe_combine_grad_bf16(tokens, k, cols, rows, dC, lddc, Y, ldy, slots, gates, dY, lddy,
+                               dgates, stream=0) -> int:
+    return load().gemm_moe_combine_grad_bf16(tokens, k, cols, rows, dC, lddc, Y, ldy, slots, gates,
+                                             dY, lddy, dgates, stream)
 
 
 def gemm_plan(elem_bytes, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, variant=0) -> int:
@@ -399,3 +521,190 @@ def grouped_wgrad(X, dY, dW, offsets, alpha: float = 1.0, beta: float = 0.0, str
     fn = gemm_bf16_grouped_wgrad if dW.dtype == torch.bfloat16 else gemm_bf16_grouped_wgrad_f32
     _check(fn(E, M, N, K, float(alpha), X.data_ptr(), _ld2(X), dY.data_ptr(), _ld2(dY), float(beta),
               dW.data_ptr(), _ld2(dW), dW.stride(0), offsets.data_ptr(), _stream_handle(stream)))
+
+
+def _flat(name: str, t, dtypes, shape) -> None:
+    """Check an operand that is held without gaps."""
+    _want(name, t, dtypes, len(shape), shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _like(name: str, t, X) -> None:
+    _want(name, t, (X.dtype,), 2, tuple(X.shape))
+
+
+def _row_ld(t) -> int:
+    return 0 if t is None else _ld2(t)
+
+
+def layernorm(X, Y, weight=None, bias=None, eps: float = 1e-5, mean=None, rstd=None,
+              stream=None) -> None:
+    """Y <- (X - mean) rstd weight + bias for each row of X (bf16 or fp32;
+    weight and bias of its type). mean and rstd (fp32, one a row) receive what
+    layernorm_grad takes. Y may be X."""
+    import torch
+    _want("X", X, (torch.bfloat16, torch.float32), 2)
+    _like("Y", Y, X)
+    rows, cols = X.shape
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _want(name, t, (X.dtype,), 1, (cols,))
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t is not None:
+            _want(name, t, (torch.float32,), 1, (rows,))
+    fn = gemm_layernorm_bf16 if X.dtype == torch.bfloat16 else gemm_layernorm_f32
+    _check(fn(rows, cols, float(eps), X.data_ptr(), _ld2(X), _ptr(weight), _ptr(bias), Y.data_ptr(),
+              _ld2(Y), _ptr(mean), _ptr(rstd), _stream_handle(stream)))
+
+
+def layernorm_grad(X, dY, dX, mean, rstd, weight=None, R=None, dweight=None, dbias=None,
+                   beta: float = 0.0, workspace=None, stream=None) -> None:
+    """dX <- R + the norm's gradient; dweight, dbias (fp32) <- beta times
+    themselves + their gradients, which needs a workspace (uint8, of
+    gemm_layernorm_grad_workspace_size(rows, cols) values). dX may be dY or R."""
+    import torch
+    _want("X", X, (torch.bfloat16, torch.float32), 2)
+    rows, cols = X.shape
+    for name, t in (("dY", dY), ("dX", dX), ("R", R)):
+        if t is not None:
+            _like(name, t, X)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _want(name, t, (torch.float32,), 1, (rows,))
+    if weight is not None:
+        _want("weight", weight, (X.dtype,), 1, (cols,))
+    for name, t in (("dweight", dweight), ("dbias", dbias)):
+        if t is not None:
+            _want(name, t, (torch.float32,), 1, (cols,))
+    if workspace is not None:
+        _want("workspace", workspace, (torch.uint8,), 1)
+    fn = gemm_layernorm_grad_bf16 if X.dtype == torch.bfloat16 else gemm_layernorm_grad_f32
+    _check(fn(rows, cols, X.data_ptr(), _ld2(X), _ptr(weight), mean.data_ptr(), rstd.data_ptr(),
+              dY.data_ptr(), _ld2(dY), _ptr(R), _row_ld(R), dX.data_ptr(), _ld2(dX), float(beta),
+              _ptr(dweight), _ptr(dbias), _ptr(workspace),
+              0 if workspace is None else workspace.numel(), _stream_handle(stream)))
+
+
+def dropout(X, Y, p: float, rng, R=None, stream=None) -> None:
+    """Y <- R + X dropped with probability p and the rest scaled by
+    1 / (1 - p). rng: 2 int64 values on the GPU, the seed and an offset that
+    the caller steps from draw to draw. The gradient is the same call on dY
+    with the same rng. Y may be X or R."""
+    import torch
+    _want("X", X, (torch.bfloat16, torch.float32), 2)
+    _like("Y", Y, X)
+    if R is not None:
+        _like("R", R, X)
+    _want("rng", rng, (torch.int64, torch.uint64), 1, (2,))
+    rows, cols = X.shape
+    fn = gemm_dropout_bf16 if X.dtype == torch.bfloat16 else gemm_dropout_f32
+    _check(fn(rows, cols, float(p), rng.data_ptr(), X.data_ptr(), _ld2(X), _ptr(R), _row_ld(R),
+              Y.data_ptr(), _ld2(Y), _stream_handle(stream)))
+
+
+def moe_route(logits, gates, choice, slots, offsets, counts, workspace, loss=None,
+              renormalize: bool = True, stream=None) -> None:
+    """The k experts of every token (logits: tokens x experts, bf16 or fp32),
+    their gates, each choice's row among the rows sorted by expert, the
+    experts' offsets there, their counts (and after them the tokens with a
+    choice) and the balance loss. gates (fp32), choice and slots (int32) are
+    tokens x k, offsets and counts experts + 1, workspace
+    gemm_moe_route_workspace_size(tokens, experts, k) values of uint8."""
+    import torch
+    _want("logits", logits, (torch.bfloat16, torch.float32), 2)
+    T, E = logits.shape
+    _want("gates", gates, (torch.float32,), 2, (T, None))
+    k = gates.shape[1]
+    _flat("gates", gates, (torch.float32,), (T, k))
+    for name, t, shape in (("choice", choice, (T, k)), ("slots", slots, (T, k)),
+                           ("offsets", offsets, (E + 1,)), ("counts", counts, (E + 1,))):
+        _flat(name, t, (torch.int32,), shape)
+    _want("workspace", workspace, (torch.uint8,), 1)
+    if loss is not None:
+        _want("loss", loss, (torch.float32,), 1, (1,))
+    fn = gemm_moe_route_bf16 if logits.dtype == torch.bfloat16 else gemm_moe_route_f32
+    _check(fn(T, E, k, int(bool(renormalize)), logits.data_ptr(), _ld2(logits), gates.data_ptr(),
+              choice.data_ptr(), slots.data_ptr(), offsets.data_ptr(), counts.data_ptr(), _ptr(loss),
+              workspace.data_ptr(), workspace.numel(), _stream_handle(stream)))
+
+
+def moe_route_grad(logits, choice, counts, dlogits, dgates=None, dloss=None,
+                   renormalize: bool = True, stream=None) -> None:
+    """dlogits <- the gradient of moe_route's gates and loss in its logits.
+    dgates: tokens x k, dloss: one value, both fp32, or None for zero."""
+    import torch
+    _want("logits", logits, (torch.bfloat16, torch.float32), 2)
+    T, E = logits.shape
+    _like("dlogits", dlogits, logits)
+    _want("choice", choice, (torch.int32,), 2, (T, None))
+    k = choice.shape[1]
+    _flat("choice", choice, (torch.int32,), (T, k))
+    _flat("counts", counts, (torch.int32,), (E + 1,))
+    if dgates is not None:
+        _flat("dgates", dgates, (torch.float32,), (T, k))
+    if dloss is not None:
+        _want("dloss", dloss, (torch.float32,), 1, (1,))
+    fn = gemm_moe_route_grad_bf16 if logits.dtype == torch.bfloat16 else gemm_moe_route_grad_f32
+    _check(fn(T, E, k, int(bool(renormalize)), logits.data_ptr(), _ld2(logits), choice.data_ptr(),
+              counts.data_ptr(), _ptr(dgates), _ptr(dloss), dlogits.data_ptr(), _ld2(dlogits),
+              _stream_handle(stream)))
+
+
+def _slots_of(slots, T: int) -> int:
+    import torch
+    _want("slots", slots, (torch.int32,), 2, (T, None))
+    _flat("slots", slots, (torch.int32,), tuple(slots.shape))
+    return slots.shape[1]
+
+
+def moe_gather(X, slots, Y, stream=None) -> None:
+    """Row slots[t, j] of Y <- row t of X, both bf16 (Y in the experts' order,
+    what matmul_bf16_grouped takes)."""
+    import torch
+    bf16 = (torch.bfloat16,)
+    _want("X", X, bf16, 2)
+    T, cols = X.shape
+    k = _slots_of(slots, T)
+    _want("Y", Y, bf16, 2, (None, cols))
+    _check(gemm_moe_gather_bf16(T, k, cols, Y.shape[0], X.data_ptr(), _ld2(X), slots.data_ptr(),
+                                Y.data_ptr(), _ld2(Y), _stream_handle(stream)))
+
+
+def moe_combine(Y, slots, C, gates=None, R=None, stream=None) -> None:
+    """Row t of C <- row t of R + the sum over j of gates[t, j] (1 without
+    gates: moe_gather's gradient) times row slots[t, j] of Y. C may be R."""
+    import torch
+    bf16 = (torch.bfloat16,)
+    _want("C", C, bf16, 2)
+    T, cols = C.shape
+    k = _slots_of(slots, T)
+    _want("Y", Y, bf16, 2, (None, cols))
+    if gates is not None:
+        _flat("gates", gates, (torch.float32,), (T, k))
+    if R is not None:
+        _like("R", R, C)
+    _check(gemm_moe_combine_bf16(T, k, cols, Y.shape[0], Y.data_ptr(), _ld2(Y), slots.data_ptr(),
+                                 _ptr(gates), _ptr(R), _row_ld(R), C.data_ptr(), _ld2(C),
+                                 _stream_handle(stream)))
+
+
+def moe_combine_grad(dC, slots, dY, Y=None, gates=None, dgates=None, stream=None) -> None:
+    """moe_combine's gradients: row slots[t, j] of dY <- gates[t, j] times row t
+    of dC, and dgates[t, j] <- the product of row t of dC and row slots[t, j] of
+    Y (Y is needed for dgates alone). dY may be Y."""
+    import torch
+    bf16 = (torch.bfloat16,)
+    _want("dC", dC, bf16, 2)
+    T, cols = dC.shape
+    k = _slots_of(slots, T)
+    _want("dY", dY, bf16, 2, (None, cols))
+    if dgates is not None:
+        _want("Y", Y, bf16, 2, (dY.shape[0], cols))
+        _flat("dgates", dgates, (torch.float32,), (T, k))
+    if gates is not None:
+        _flat("gates", gates, (torch.float32,), (T, k))
+    _check(gemm_moe_combine_grad_bf16(T, k, cols, dY.shape[0], dC.data_ptr(), _ld2(dC),
+                                      _ptr(Y) if dgates is not None else None,
+                                      _row_ld(Y) if dgates is not None else 0, slots.data_ptr(),
+                                      _ptr(gates), dY.data_ptr(), _ld2(dY), _ptr(dgates),
+                                      _stream_handle(stream)))

@@ -5,12 +5,14 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cfloat>
 #include <climits>
 #include <cstring>
 
 #include "gemm.h"
 #include "common.hpp"
 #include "kernels.hpp"
+#include "layer.hpp"
 #include "ops.hpp"
 
 namespace {
@@ -667,6 +669,247 @@ gemm_status_t gemm_bf16_grouped_wgrad_f32(int64_t groups, int64_t M, int64_t N, 
                                           float* dW, int64_t lddw, int64_t stridedw, const int32_t* offsets,
                                           void* stream) {
     return grouped_wgrad(true, groups, M, N, K, alpha, X, ldx, dY, lddy, beta, dW, lddw, stridedw, offsets, stream);
+}
+
+}  // extern "C"
+
+// ---- around the products of an expert-routed layer -------------------------------
+
+namespace {
+
+// A rows x cols operand with its leading dimension.
+bool matrix_ok(int esz, int64_t rows, int64_t cols, const void* p, int64_t ld) {
+    return ld >= max1(cols) && span_ok(esz, rows, cols, ld) && aligned(p, esz);
+}
+
+// A workspace that the call needs.
+bool scratch_ok(const void* ws, size_t bytes, size_t need) { return ws != nullptr && aligned(ws, 256) && bytes >= need; }
+
+template <typename T>
+gemm_status_t layernorm(int64_t rows, int64_t cols, float eps, const T* X, int64_t ldx, const T* weight, const T* bias,
+                        T* Y, int64_t ldy, float* mean, float* rstd, void* stream) {
+    constexpr int esz = sizeof(T);
+    if (!size_ok(rows) || !size_ok(cols) || !(eps >= 0.f && eps <= FLT_MAX)) return GEMM_ERR_INVALID_VALUE;
+    if (!matrix_ok(esz, rows, cols, X, ldx) || !matrix_ok(esz, rows, cols, Y, ldy)) return GEMM_ERR_INVALID_VALUE;
+    if (!aligned(weight, esz) || !aligned(bias, esz) || !aligned(mean, 4) || !aligned(rstd, 4))
+        return GEMM_ERR_INVALID_VALUE;
+    if (rows == 0 || cols == 0) return GEMM_OK;
+    if (X == nullptr || Y == nullptr) return GEMM_ERR_INVALID_VALUE;
+    const dg::NormArgs<T> a{rows, cols, eps, X, ldx, weight, bias, Y, ldy, mean, rstd};
+    return on_device([&](int cus) { return dg::launch_layernorm(a, cus, reinterpret_cast<hipStream_t>(stream)); });
+}
+
+template <typename T>
+gemm_status_t layernorm_grad(int64_t rows, int64_t cols, const T* X, int64_t ldx, const T* weight, const float* mean,
+                             const float* rstd, const T* dY, int64_t lddy, const T* R, int64_t ldr, T* dX, int64_t lddx,
+                             float beta, float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+    constexpr int esz = sizeof(T);
+    if (!size_ok(rows) || !size_ok(cols)) return GEMM_ERR_INVALID_VALUE;
+    if (!matrix_ok(esz, rows, cols, X, ldx) || !matrix_ok(esz, rows, cols, dY, lddy) ||
+        !matrix_ok(esz, rows, cols, dX, lddx) || (R != nullptr && !matrix_ok(esz, rows, cols, R, ldr)))
+        return GEMM_ERR_INVALID_VALUE;
+    if (!aligned(weight, esz) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dweight, 4) || !aligned(dbias, 4))
+        return GEMM_ERR_INVALID_VALUE;
+    const bool columns = dweight != nullptr || dbias != nullptr;
+    if (workspace == nullptr && workspace_bytes != 0) return GEMM_ERR_INVALID_VALUE;
+    if (cols == 0 || (rows == 0 && (!columns || beta == 1.f))) return GEMM_OK;
+    if (rows > 0 && (X == nullptr || mean == nullptr || rstd == nullptr || dY == nullptr || dX == nullptr))
+        return GEMM_ERR_INVALID_VALUE;
+    if (columns && !scratch_ok(workspace, workspace_bytes, dg::layernorm_grad_workspace(rows, cols)))
+        return GEMM_ERR_INVALID_VALUE;
+    const dg::NormGradArgs<T> a{rows, cols, X, ldx, weight, mean, rstd, dY, lddy, R, ldr, dX, lddx, beta, dweight,
+                                dbias, static_cast<float*>(workspace)};
+    return on_device([&](int) { return dg::launch_layernorm_grad(a, reinterpret_cast<hipStream_t>(stream)); });
+}
+
+template <typename T>
+gemm_status_t dropout(int64_t rows, int64_t cols, float p, const uint64_t* rng, const T* X, int64_t ldx, const T* R,
+                      int64_t ldr, T* Y, int64_t ldy, void* stream) {
+    constexpr int esz = sizeof(T);
+    if (!size_ok(rows) || !size_ok(cols) || !(p >= 0.f && p <= 1.f)) return GEMM_ERR_INVALID_VALUE;
+    if (!matrix_ok(esz, rows, cols, X, ldx) || !matrix_ok(esz, rows, cols, Y, ldy) ||
+        (R != nullptr && !matrix_ok(esz, rows, cols, R, ldr)) || !aligned(rng, 8))
+        return GEMM_ERR_INVALID_VALUE;
+    if (rows == 0 || cols == 0) return GEMM_OK;
+    if (X == nullptr || Y == nullptr || rng == nullptr) return GEMM_ERR_INVALID_VALUE;
+    const dg::DropoutArgs<T> a{rows, cols, (uint32_t)(p * 65536.f + 0.5f), rng, X, ldx, R, ldr, Y, ldy};
+    return on_device([&](int) { return dg::launch_dropout(a, reinterpret_cast<hipStream_t>(stream)); });
+}
+
+bool choices_ok(int64_t tokens, int k, int64_t most) {
+    return size_ok(tokens) && k >= 1 && k <= most && tokens * k <= INT_MAX;
+}
+
+bool route_sizes_ok(int64_t tokens, int64_t experts, int k) {
+    return experts >= 1 && experts <= GEMM_MOE_MAX_EXPERTS &&
+           choices_ok(tokens, k, experts < GEMM_MOE_MAX_K ? experts : GEMM_MOE_MAX_K);
+}
+
+template <typename T>
+gemm_status_t moe_route(int64_t tokens, int64_t experts, int k, int renormalize, const T* logits, int64_t ldl,
+                        float* gates, int32_t* choice, int32_t* slots, int32_t* offsets, int32_t* counts, float* loss,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+    if (!route_sizes_ok(tokens, experts, k) || !matrix_ok(sizeof(T), tokens, experts, logits, ldl))
+        return GEMM_ERR_INVALID_VALUE;
+    if (!aligned(gates, 4) || !aligned(choice, 4) || !aligned(slots, 4) || !aligned(offsets, 4) || !aligned(counts, 4) ||
+        !aligned(loss, 4))
+        return GEMM_ERR_INVALID_VALUE;
+    if (offsets == nullptr || counts == nullptr) return GEMM_ERR_INVALID_VALUE;
+    if (tokens > 0 && (logits == nullptr || gates == nullptr || choice == nullptr || slots == nullptr))
+        return GEMM_ERR_INVALID_VALUE;
+    if (!scratch_ok(workspace, workspace_bytes, dg::route_workspace(tokens, experts, k))) return GEMM_ERR_INVALID_VALUE;
+    const dg::RouteArgs<T> a{(int)tokens, (int)experts, k, renormalize != 0, logits, ldl, gates, choice, slots, offsets,
+                             counts, loss, workspace};
+    return on_device([&](int) { return dg::launch_route(a, reinterpret_cast<hipStream_t>(stream)); });
+}
+
+template <typename T>
+gemm_status_t moe_route_grad(int64_t tokens, int64_t experts, int k, int renormalize, const T* logits, int64_t ldl,
+                             const int32_t* choice, const int32_t* counts, const float* dgates, const float* dloss,
+                             T* dlogits, int64_t lddl, void* stream) {
+    if (!route_sizes_ok(tokens, experts, k) || !matrix_ok(sizeof(T), tokens, experts, logits, ldl) ||
+        !matrix_ok(sizeof(T), tokens, experts, dlogits, lddl))
+        return GEMM_ERR_INVALID_VALUE;
+    if (!aligned(choice, 4) || !aligned(counts, 4) || !aligned(dgates, 4) || !aligned(dloss, 4))
+        return GEMM_ERR_INVALID_VALUE;
+    if (tokens == 0) return GEMM_OK;
+    if (logits == nullptr || choice == nullptr || counts == nullptr || dlogits == nullptr) return GEMM_ERR_INVALID_VALUE;
+    const dg::RouteGradArgs<T> a{(int)tokens, (int)experts, k, renormalize != 0, logits, ldl, choice, counts, dgates,
+                                 dloss, dlogits, lddl};
+    return on_device([&](int) { return dg::launch_route_grad(a, reinterpret_cast<hipStream_t>(stream)); });
+}
+
+// What the three row calls check alike: the tokens' matrix, the sorted one, the slots.
+bool rows_ok(int64_t tokens, int k, int64_t cols, int64_t rows, const void* mine, int64_t ldm, const void* sorted,
+             int64_t lds, const int32_t* slots, const float* gates) {
+    return choices_ok(tokens, k, GEMM_MOE_MAX_K) && size_ok(cols) && size_ok(rows) &&
+           matrix_ok(2, tokens, cols, mine, ldm) && matrix_ok(2, rows, cols, sorted, lds) && aligned(slots, 4) &&
+           aligned(gates, 4);
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_layernorm_bf16(int64_t rows, int64_t cols, float eps, const uint16_t* X, int64_t ldx,
+                                  const uint16_t* weight, const uint16_t* bias, uint16_t* Y, int64_t ldy, float* mean,
+                                  float* rstd, void* stream) {
+    return layernorm<uint16_t>(rows, cols, eps, X, ldx, weight, bias, Y, ldy, mean, rstd, stream);
+}
+
+gemm_status_t gemm_layernorm_f32(int64_t rows, int64_t cols, float eps, const float* X, int64_t ldx,
+                                 const float* weight, const float* bias, float* Y, int64_t ldy, float* mean,
+                                 float* rstd, void* stream) {
+    return layernorm<float>(rows, cols, eps, X, ldx, weight, bias, Y, ldy, mean, rstd, stream);
+}
+
+size_t gemm_layernorm_grad_workspace_size(int64_t rows, int64_t cols) {
+    return size_ok(rows) && size_ok(cols) ? dg::layernorm_grad_workspace(rows, cols) : 0;
+}
+
+gemm_status_t gemm_layernorm_grad_bf16(int64_t rows, int64_t cols, const uint16_t* X, int64_t ldx,
+                                       const uint16_t* weight, const float* mean, const float* rstd, const uint16_t* dY,
+                                       int64_t lddy, const uint16_t* R, int64_t ldr, uint16_t* dX, int64_t lddx,
+                                       float beta, float* dweight, float* dbias, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+    return layernorm_grad<uint16_t>(rows, cols, X, ldx, weight, mean, rstd, dY, lddy, R, ldr, dX, lddx, beta, dweight,
+                                    dbias, workspace, workspace_bytes, stream);
+}
+
+gemm_status_t gemm_layernorm_grad_f32(int64_t rows, int64_t cols, const float* X, int64_t ldx, const float* weight,
+                                      const float* mean, const float* rstd, const float* dY, int64_t lddy,
+                                      const float* R, int64_t ldr, float* dX, int64_t lddx, float beta, float* dweight,
+                                      float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+    return layernorm_grad<float>(rows, cols, X, ldx, weight, mean, rstd, dY, lddy, R, ldr, dX, lddx, beta, dweight,
+                                 dbias, workspace, workspace_bytes, stream);
+}
+
+gemm_status_t gemm_dropout_bf16(int64_t rows, int64_t cols, float p, const uint64_t* rng, const uint16_t* X,
+                                int64_t ldx, const uint16_t* R, int64_t ldr, uint16_t* Y, int64_t ldy, void* stream) {
+    return dropout<uint16_t>(rows, cols, p, rng, X, ldx, R, ldr, Y, ldy, stream);
+}
+
+gemm_status_t gemm_dropout_f32(int64_t rows, int64_t cols, float p, const uint64_t* rng, const float* X, int64_t ldx,
+                               const float* R, int64_t ldr, float* Y, int64_t ldy, void* stream) {
+    return dropout<float>(rows, cols, p, rng, X, ldx, R, ldr, Y, ldy, stream);
+}
+
+size_t gemm_moe_route_workspace_size(int64_t tokens, int64_t experts, int k) {
+    return route_sizes_ok(tokens, experts, k) ? dg::route_workspace(tokens, experts, k) : 0;
+}
+
+gemm_status_t gemm_moe_route_bf16(int64_t tokens, int64_t experts, int k, int renormalize, const uint16_t* logits,
+                                  int64_t ldl, float* gates, int32_t* choice, int32_t* slots, int32_t* offsets,
+                                  int32_t* counts, float* loss, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+    return moe_route<uint16_t>(tokens, experts, k, renormalize, logits, ldl, gates, choice, slots, offsets, counts, loss,
+                               workspace, workspace_bytes, stream);
+}
+
+gemm_status_t gemm_moe_route_f32(int64_t tokens, int64_t experts, int k, int renormalize, const float* logits,
+                                 int64_t ldl, float* gates, int32_t* choice, int32_t* slots, int32_t* offsets,
+                                 int32_t* counts, float* loss, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+    return moe_route<float>(tokens, experts, k, renormalize, logits, ldl, gates, choice, slots, offsets, counts, loss,
+                            workspace, workspace_bytes, stream);
+}
+
+gemm_status_t gemm_moe_route_grad_bf16(int64_t tokens, int64_t experts, int k, int renormalize, const uint16_t* logits,
+                                       int64_t ldl, const int32_t* choice, const int32_t* counts, const float* dgates,
+                                       const float* dloss, uint16_t* dlogits, int64_t lddl, void* stream) {
+    return moe_route_grad<uint16_t>(tokens, experts, k, renormalize, logits, ldl, choice, counts, dgates, dloss, dlogits,
+                                    lddl, stream);
+}
+
+gemm_status_t gemm_moe_route_grad_f32(int64_t tokens, int64_t experts, int k, int renormalize, const float* logits,
+                                      int64_t ldl, const int32_t* choice, const int32_t* counts, const float* dgates,
+                                      const float* dloss, float* dlogits, int64_t lddl, void* stream) {
+    return moe_route_grad<float>(tokens, experts, k, renormalize, logits, ldl, choice, counts, dgates, dloss, dlogits,
+                                 lddl, stream);
+}
+
+gemm_status_t gemm_moe_gather_bf16(int64_t tokens, int k, int64_t cols, int64_t rows, const uint16_t* X, int64_t ldx,
+                                   const int32_t* slots, uint16_t* Y, int64_t ldy, void* stream) {
+    if (!rows_ok(tokens, k, cols, rows, X, ldx, Y, ldy, slots, nullptr)) return GEMM_ERR_INVALID_VALUE;
+    if (tokens == 0 || cols == 0 || rows == 0) return GEMM_OK;
+    if (X == nullptr || slots == nullptr || Y == nullptr) return GEMM_ERR_INVALID_VALUE;
+    dg::RowsArgs a{tokens, cols, rows, k, slots};
+    a.X = X; a.ldx = ldx;
+    a.out = Y; a.ldo = ldy;
+    return on_device([&](int) { return dg::launch_gather(a, reinterpret_cast<hipStream_t>(stream)); });
+}
+
+gemm_status_t gemm_moe_combine_bf16(int64_t tokens, int k, int64_t cols, int64_t rows, const uint16_t* Y, int64_t ldy,
+                                    const int32_t* slots, const float* gates, const uint16_t* R, int64_t ldr,
+                                    uint16_t* C, int64_t ldc, void* stream) {
+    if (!rows_ok(tokens, k, cols, rows, C, ldc, Y, ldy, slots, gates)) return GEMM_ERR_INVALID_VALUE;
+    if (R != nullptr && !matrix_ok(2, tokens, cols, R, ldr)) return GEMM_ERR_INVALID_VALUE;
+    if (tokens == 0 || cols == 0) return GEMM_OK;
+    if (C == nullptr || slots == nullptr || (Y == nullptr && rows > 0)) return GEMM_ERR_INVALID_VALUE;
+    dg::RowsArgs a{tokens, cols, rows, k, slots, gates};
+    a.X = R; a.ldx = ldr;
+    a.Y = Y; a.ldy = ldy;
+    a.out = C; a.ldo = ldc;
+    return on_device([&](int) { return dg::launch_combine(a, reinterpret_cast<hipStream_t>(stream)); });
+}
+
+gemm_status_t gemm_moe_combine_grad_bf16(int64_t tokens, int k, int64_t cols, int64_t rows, const uint16_t* dC,
+                                         int64_t lddc, const uint16_t* Y, int64_t ldy, const int32_t* slots,
+                                         const float* gates, uint16_t* dY, int64_t lddy, float* dgates,
+                                         void* stream) {
+    if (!rows_ok(tokens, k, cols, rows, dC, lddc, dY, lddy, slots, gates) || !aligned(dgates, 4))
+        return GEMM_ERR_INVALID_VALUE;
+    if (dgates != nullptr && !matrix_ok(2, rows, cols, Y, ldy)) return GEMM_ERR_INVALID_VALUE;
+    if (tokens == 0 || (dgates == nullptr && (cols == 0 || rows == 0))) return GEMM_OK;
+    if (slots == nullptr || (cols > 0 && dC == nullptr)) return GEMM_ERR_INVALID_VALUE;
+    if (cols > 0 && rows > 0 && (dY == nullptr || (dgates != nullptr && Y == nullptr))) return GEMM_ERR_INVALID_VALUE;
+    dg::RowsArgs a{tokens, cols, rows, k, slots, gates};
+    a.X = dC; a.ldx = lddc;
+    a.Y = Y; a.ldy = ldy;
+    a.out = dY; a.ldo = lddy;
+    a.dgates = dgates;
+    return on_device([&](int) { return dg::launch_combine_grad(a, reinterpret_cast<hipStream_t>(stream)); });
 }
 
 }  // extern "C"

@@ -480,6 +480,163 @@ gemm_status_t gemm_bf16_grouped_wgrad_f32(int64_t groups, int64_t M, int64_t N, 
                                           float beta, float* dW, int64_t lddw, int64_t stridedw,
                                           const int32_t* offsets, void* stream);
 
+/* ---- Around the products of an expert-routed layer ---------------------------
+ *
+ * What stands before and behind such products in a transformer: layer norm,
+ * dropout, the router that sorts rows by expert, and the rows' way into that
+ * order and back, with their gradients. Matrices are row-major with a leading
+ * dimension as everywhere here; every alignment is taken, and rows on 16 bytes
+ * are the fastest. Everything between the operands and a result is formed in
+ * fp32 and rounded once. No call uses atomics: the same call gives the same bits.
+ * Streams, errors and ownership are those of the other calls. An output may be
+ * the same matrix (base and leading dimension) as an input only where said;
+ * other overlaps give undefined results.
+ *
+ * Layer norm of each row of X (rows x cols), with m its mean and
+ * r = 1 / sqrt(mean of (x - m)^2 + eps):
+ *
+ *     Y(i,j) <- (X(i,j) - m_i) * r_i * weight[j] + bias[j]
+ *
+ * weight, bias: cols values of X's type, or NULL for 1 and 0. mean, rstd: rows
+ * fp32 values each, which receive m and r for the gradient, or NULL. Y may be X.
+ * eps >= 0 (finite); a constant row with eps == 0 has r = infinity, and NaN in
+ * Y. A row that holds an infinity or a NaN gets NaN. The mean is taken first and the squares of
+ * the differences from it then, so rows far from zero lose nothing. rows == 0 or
+ * cols == 0 does nothing. */
+gemm_status_t gemm_layernorm_bf16(int64_t rows, int64_t cols, float eps, const uint16_t* X, int64_t ldx,
+                                  const uint16_t* weight, const uint16_t* bias, uint16_t* Y, int64_t ldy,
+                                  float* mean, float* rstd, void* stream);
+gemm_status_t gemm_layernorm_f32(int64_t rows, int64_t cols, float eps, const float* X, int64_t ldx,
+                                 const float* weight, const float* bias, float* Y, int64_t ldy,
+                                 float* mean, float* rstd, void* stream);
+
+/* Its gradients. With h = (x - m) r and g = dY * weight, for each row
+ *
+ *     dX(i,j) <- R(i,j) + r_i * (g(i,j) - mean_j g(i,:) - h(i,j) * mean_j (g h)(i,:))
+ *
+ * and for each column
+ *
+ *     dweight[j] <- beta * dweight[j] + sum_i dY(i,j) h(i,j),
+ *     dbias[j]   <- beta * dbias[j]   + sum_i dY(i,j)
+ *
+ * R: the gradient that reaches X past the norm (the residual path's), or NULL.
+ * dX may be dY or R. dweight, dbias: cols fp32 values each, or NULL when not
+ * wanted; beta == 0 does not read them; rows == 0 leaves beta times them.
+ * mean, rstd: what the forward call gave. workspace: device memory of at least
+ * gemm_layernorm_grad_workspace_size(rows, cols) bytes, 256-byte aligned, whose
+ * contents do not matter before or after; NULL (and size 0) when neither dweight
+ * nor dbias is wanted. Calls that share one must not overlap in time. */
+size_t gemm_layernorm_grad_workspace_size(int64_t rows, int64_t cols);
+gemm_status_t gemm_layernorm_grad_bf16(int64_t rows, int64_t cols, const uint16_t* X, int64_t ldx,
+                                       const uint16_t* weight, const float* mean, const float* rstd,
+                                       const uint16_t* dY, int64_t lddy, const uint16_t* R, int64_t ldr,
+                                       uint16_t* dX, int64_t lddx, float beta, float* dweight, float* dbias,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+gemm_status_t gemm_layernorm_grad_f32(int64_t rows, int64_t cols, const float* X, int64_t ldx,
+                                      const float* weight, const float* mean, const float* rstd,
+                                      const float* dY, int64_t lddy, const float* R, int64_t ldr,
+                                      float* dX, int64_t lddx, float beta, float* dweight, float* dbias,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Dropout, with a residual:
+ *
+ *     Y(i,j) <- R(i,j) + (u(i,j) >= t ? X(i,j) * 65536 / (65536 - t) : 0),   t = p * 65536 to nearest
+ *
+ * u: 16 bits of a counter-based generator (Philox 4x32 of 10 rounds: Salmon et
+ * al., "Parallel random numbers: as easy as 1, 2, 3"), drawn anew wherever the
+ * mask is needed: key (rng[0] low, high word), counter (j / 8, i, rng[1] low,
+ * high word); of its words w0 .. w3, column j takes the low (j even) or high half
+ * of w[j % 8 / 2]. rng: device pointer to the seed and the offset (8-byte
+ * aligned), read by the kernel, so a captured call follows them at each replay;
+ * the caller steps the offset between draws. A mask depends on nothing but
+ * rng, i and j: not on the type, leading dimensions or alignment. The gradient
+ * is the same call on dY with the same rng, and R the residual path's gradient.
+ * p in [0, 1]: 0 keeps everything, 1 drops everything (a t of 65536). A dropped
+ * element counts as 0 whatever X holds. R may be NULL; Y may be X or R. */
+gemm_status_t gemm_dropout_bf16(int64_t rows, int64_t cols, float p, const uint64_t* rng, const uint16_t* X,
+                                int64_t ldx, const uint16_t* R, int64_t ldr, uint16_t* Y, int64_t ldy,
+                                void* stream);
+gemm_status_t gemm_dropout_f32(int64_t rows, int64_t cols, float p, const uint64_t* rng, const float* X,
+                               int64_t ldx, const float* R, int64_t ldr, float* Y, int64_t ldy, void* stream);
+
+/* Router: every token's k experts, the rows' order by expert, and the balance
+ * loss. logits: tokens x experts; p = softmax of a token's logits.
+ *
+ *   choice[t*k + j]  the expert of the j-th largest logit of token t (of equal
+ *                    ones the lower expert first)
+ *   gates[t*k + j]   its p, or with renormalize != 0 its p over the sum of the
+ *                    token's chosen ones
+ *   counts[e]        rows of expert e; counts[experts]: tokens with a choice
+ *   offsets[e]       rows of the experts before e; offsets[experts]: all rows
+ *                    (what gemm_bf16_grouped takes)
+ *   slots[t*k + j]   the row that choice takes among the sorted ones: by expert,
+ *                    an expert's rows by token
+ *   loss[0]          experts * sum_e (counts[e] / all rows) * (sum_t p(t,e) / tokens
+ *                    with a choice): 1 when balanced
+ *
+ * A logit of -infinity is never chosen; where a token has fewer than k others its
+ * last choices and slots are -1, their gates 0. A token of -infinities alone
+ * (padding) has no choice and no part in the loss, which is 0 without any token.
+ * A token that holds a NaN or +infinity has no choice, gates of NaN, and makes
+ * the loss NaN. loss may be NULL (serving). experts: 1 .. GEMM_MOE_MAX_EXPERTS, k: 1 ..
+ * min(experts, GEMM_MOE_MAX_K), tokens * k <= INT_MAX. workspace: as for the norm's
+ * gradient, gemm_moe_route_workspace_size bytes (0 for invalid sizes). */
+#define GEMM_MOE_MAX_EXPERTS 1024
+#define GEMM_MOE_MAX_K 16
+size_t gemm_moe_route_workspace_size(int64_t tokens, int64_t experts, int k);
+gemm_status_t gemm_moe_route_bf16(int64_t tokens, int64_t experts, int k, int renormalize, const uint16_t* logits,
+                                  int64_t ldl, float* gates, int32_t* choice, int32_t* slots, int32_t* offsets,
+                                  int32_t* counts, float* loss, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+gemm_status_t gemm_moe_route_f32(int64_t tokens, int64_t experts, int k, int renormalize, const float* logits,
+                                 int64_t ldl, float* gates, int32_t* choice, int32_t* slots, int32_t* offsets,
+                                 int32_t* counts, float* loss, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* The gradient of gates and loss in the logits (choices and counts are
+ * constants): with a(e) = dloss * experts * counts[e] / (all rows * tokens with
+ * a choice), d the gradient of a choice's gate and q the token's gates,
+ *
+ *     dlogits(t,e) <- p(t,e) * (a(e) - sum_i a(i) p(t,i))
+ *                     + sum over j with choice e of q_j * (d_j - s)        (renormalised,   s = sum_i d_i q_i)
+ *                     or, without, a(e) takes d_j too
+ *
+ * choice, counts: as gemm_moe_route gave them. dgates (tokens x k) or dloss (one
+ * fp32 value on the device) may be NULL for zero; dgates of absent choices are
+ * not read into any sum. dlogits may be logits. */
+gemm_status_t gemm_moe_route_grad_bf16(int64_t tokens, int64_t experts, int k, int renormalize,
+                                       const uint16_t* logits, int64_t ldl, const int32_t* choice,
+                                       const int32_t* counts, const float* dgates, const float* dloss,
+                                       uint16_t* dlogits, int64_t lddl, void* stream);
+gemm_status_t gemm_moe_route_grad_f32(int64_t tokens, int64_t experts, int k, int renormalize,
+                                      const float* logits, int64_t ldl, const int32_t* choice,
+                                      const int32_t* counts, const float* dgates, const float* dloss,
+                                      float* dlogits, int64_t lddl, void* stream);
+
+/* Rows into the experts' order and back. slots: tokens x k, as gemm_moe_route
+ * gives them; a slot outside [0, rows) counts as absent. rows: those that the
+ * sorted matrix Y (or dY) is allocated with; ones that no slot names are neither
+ * read nor written. k: 1 .. GEMM_MOE_MAX_K.
+ *
+ *   gather:        Y(slot_tj,:) <- X(t,:)                  two equal slots leave either's row
+ *   combine:       C(t,:) <- R(t,:) + sum_j gates[t,j] * Y(slot_tj,:)
+ *   its gradient:  dY(slot_tj,:) <- gates[t,j] * dC(t,:),
+ *                  dgates[t,j] <- sum over columns of dC(t,:) * Y(slot_tj,:)
+ *
+ * The gradient of gather is combine with gates NULL (1). An absent slot's term is
+ * 0 * gates[t,j] (so that a router's NaN shows) and its dgates 0. R may be NULL, and C may be R.
+ * dgates may be NULL, and then Y too; with gates NULL dY takes dC itself. dY may be Y.
+ * k terms are summed in the order of j. */
+gemm_status_t gemm_moe_gather_bf16(int64_t tokens, int k, int64_t cols, int64_t rows, const uint16_t* X,
+                                   int64_t ldx, const int32_t* slots, uint16_t* Y, int64_t ldy, void* stream);
+gemm_status_t gemm_moe_combine_bf16(int64_t tokens, int k, int64_t cols, int64_t rows, const uint16_t* Y,
+                                    int64_t ldy, const int32_t* slots, const float* gates, const uint16_t* R,
+                                    int64_t ldr, uint16_t* C, int64_t ldc, void* stream);
+gemm_status_t gemm_moe_combine_grad_bf16(int64_t tokens, int k, int64_t cols, int64_t rows, const uint16_t* dC,
+                                         int64_t lddc, const uint16_t* Y, int64_t ldy, const int32_t* slots,
+                                         const float* gates, uint16_t* dY, int64_t lddy, float* dgates,
+                                         void* stream);
+
 /* Host-only planning (no HIP call): the variant a call with these arguments
  * would run (a gemm_variant_t value; GEMM_VARIANT_AUTO when the call would
  * launch no GEMM kernel), or -1 when the arguments are invalid. `elem_bytes`
