@@ -138,8 +138,9 @@ struct Vec<uint16_t> {
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (e < valid) p[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+            if (e < valid) store1(p + e, e);
     }
+    __device__ __forceinline__ void store1(uint16_t* p, int e) const { *p = (uint16_t)(w[e >> 1] >> (16 * (e & 1))); }
 };
 template <>
 struct Vec<float> {
@@ -167,6 +168,7 @@ struct Vec<float> {
         for (int e = 0; e < 4; ++e)
             if (e < valid) p[e] = w[e];
     }
+    __device__ __forceinline__ void store1(float* p, int e) const { *p = w[e]; }
 };
 
 // Elements of a vector at column c0 that lie inside a row of `cols`.
@@ -175,11 +177,35 @@ __device__ __forceinline__ int inside(int64_t cols, int64_t c0, int n) {
     return left >= n ? n : (left > 0 ? (int)left : 0);
 }
 
-// Sum over the wave, in every lane.
+// Where a lane's vector at column c of a row of `cols` >= n values is read: the
+// last n of the row where it would pass their end, so that no lane reads
+// element by element; its first `skip` elements then belong to the vector
+// before (all of them where c lies past the end).
+struct LastVec {
+    int from, skip;
+};
+__device__ __forceinline__ LastVec last_vec(int cols, int c, int n) {
+    const int from = c + n <= cols ? c : cols - n;
+    return LastVec{from, c - from < n ? c - from : n};
+}
+
+// Lane exchanges that the vector unit does on its own (DPP): sums over 16
+// neighbouring lanes, in all of them, and over the wave, as a scalar.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ float sum_of_16(float v) {
+    v = dpp_add<0xB1, 0xf>(v);         // lane ^ 1
+    v = dpp_add<0x4E, 0xf>(v);         // lane ^ 2
+    v = dpp_add<0x141, 0xf>(v);        // mirrored in 8
+    return dpp_add<0x140, 0xf>(v);     // mirrored in 16
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
-    return v;
+    v = sum_of_16(v);
+    v = dpp_add<0x142, 0xa>(v);        // rows 1 and 3 take the row before
+    v = dpp_add<0x143, 0xc>(v);        // rows 2 and 3 take the first half
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
 // Workgroups for `units` independent pieces: as many, up to what a grid

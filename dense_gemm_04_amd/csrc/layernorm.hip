@@ -134,20 +134,268 @@ __global__ __launch_bounds__(256) void norm_grad_cols(NormGradArgs<T> a) {
     }
 }
 
+// Both at once, in one pass over X and dY: L threads to a row (16, or whole
+// waves), V vectors to a thread, which keeps the row's values in registers
+// between the row's sums and dX, and its columns' sums of dY h and dY in 2 V n
+// more. A workgroup of 512 threads takes 512 / L rows at a time and adds its
+// threads' column sums up in LDS at the end, into one image of the registers
+// for each workgroup; sum_images adds those, in their order.
+template <typename T, int L, int V, bool RES>
+__global__ __launch_bounds__(512, 2) void norm_grad(NormGradArgs<T> a) {
+    constexpr int n = Vec<T>::n, kGroups = 512 / L, kWaves = L / 64;
+    constexpr int kImage = V * L * n / 4;                       // f32x4 of one sum
+    __shared__ union {
+        u32x4 w[V * L];
+        f32x4 image[kImage];
+    } lds;
+    __shared__ float part[2][8][2];
+    const int t = threadIdx.x, lane = t % L, group = t / L, wave = t >> 6;
+    const int cols = (int)a.cols;
+    int col[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) col[i] = (i * L + lane) * n;
+    const LastVec last = last_vec(cols, col[V - 1], n);
+    col[V - 1] = last.from;
+    if (group == 0) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            Vec<T> w;
+            if (a.weight != nullptr) {
+                w.load(a.weight + col[i], n);
+            } else {
+                float one[n];
+#pragma unroll
+                for (int e = 0; e < n; ++e) one[e] = 1.f;
+                w.set(one);
+            }
+            lds.w[i * L + lane] = __builtin_bit_cast(u32x4, w.w);
+        }
+    }
+    __syncthreads();
+    float dw[V][n] = {}, db[V][n] = {};
+    const float inv = 1.f / (float)cols;
+    int turn = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * kGroups; row0 < a.rows; row0 += (int64_t)gridDim.x * kGroups, turn ^= 1) {
+        const int64_t row = row0 + group;
+        const bool on = row < a.rows;
+        Vec<T> x[V], dy[V], res[V];
+        float r = 0.f, mr = 0.f, sg = 0.f, sgh = 0.f;
+        if (on) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                x[i].load(a.X + row * a.ldx + col[i], n);
+                dy[i].load(a.dY + row * a.lddy + col[i], n);
+            }
+            if constexpr (RES) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) res[i].load(a.R + row * a.ldr + col[i], n);
+            }
+            r = a.rstd[row];
+            mr = -a.mean[row];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                Vec<T> w;
+                w.w = __builtin_bit_cast(decltype(w.w), lds.w[i * L + lane]);
+#pragma unroll
+                for (int e = 0; e < n; ++e) {
+                    const float h = (x[i].at(e) + mr) * r;
+                    float d = dy[i].at(e);
+                    if (i == V - 1) d = e >= last.skip ? d : 0.f;
+                    const float g = d * w.at(e);
+                    sg += g;
+                    sgh = i == V - 1 && e < last.skip ? sgh : __builtin_fmaf(g, h, sgh);
+                    db[i][e] += d;
+                    dw[i][e] = i == V - 1 && e < last.skip ? 0.f : __builtin_fmaf(d, h, dw[i][e]);
+                }
+            }
+        }
+        if constexpr (L == 16) {
+            sg = sum_of_16(sg);
+            sgh = sum_of_16(sgh);
+        } else {
+            sg = wave_sum(sg);
+            sgh = wave_sum(sgh);
+            if constexpr (kWaves > 1) {
+                if ((t & 63) == 0) {
+                    part[turn][wave][0] = sg;
+                    part[turn][wave][1] = sgh;
+                }
+                __syncthreads();
+                sg = sgh = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) {
+                    sg += part[turn][group * kWaves + w][0];
+                    sgh += part[turn][group * kWaves + w][1];
+                }
+            }
+        }
+        if (!on) continue;
+        const float c1 = sg * inv, c2 = sgh * inv;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            Vec<T> w;
+            w.w = __builtin_bit_cast(decltype(w.w), lds.w[i * L + lane]);
+            float out[n];
+#pragma unroll
+            for (int e = 0; e < n; ++e) {
+                const float h = (x[i].at(e) + mr) * r;
+                const float in = __builtin_fmaf(-h, c2, __builtin_fmaf(dy[i].at(e), w.at(e), -c1));
+                out[e] = __builtin_fmaf(r, in, RES ? res[i].at(e) : 0.f);
+            }
+            x[i].set(out);
+            T* p = a.dX + row * a.lddx + col[i];
+            if (i < V - 1 || last.skip == 0) {
+                x[i].store(p, n);
+            } else {
+#pragma unroll
+                for (int e = 0; e < n; ++e)
+                    if (e >= last.skip) x[i].store1(p + e, e);
+            }
+        }
+    }
+    if (a.dweight == nullptr && a.dbias == nullptr) return;
+    // Rows of 16 lanes first: their sums meet within the wave.
+    constexpr int kSets = L == 16 ? 8 : kGroups;
+    const int set = L == 16 ? wave : group;
+    if constexpr (L == 16) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int e = 0; e < n; ++e) {
+                dw[i][e] += __shfl_xor(dw[i][e], 16, 64);
+                dw[i][e] += __shfl_xor(dw[i][e], 32, 64);
+                db[i][e] += __shfl_xor(db[i][e], 16, 64);
+                db[i][e] += __shfl_xor(db[i][e], 32, 64);
+            }
+    }
+    const bool mine = L != 16 || (t & 63) < 16;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        f32x4* image = reinterpret_cast<f32x4*>(a.ws) + ((int64_t)blockIdx.x * 2 + which) * kImage;
+        for (int s = 0; s < kSets; ++s) {
+            if (kSets > 1) __syncthreads();
+            if (set != s || !mine) continue;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int q = 0; q < n / 4; ++q) {
+                    const int at = (i * (n / 4) + q) * L + lane;
+                    f32x4 v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = which == 0 ? dw[i][4 * q + e] : db[i][4 * q + e];
+                    if (s > 0) v += lds.image[at];
+                    if (s < kSets - 1) lds.image[at] = v;
+                    else image[at] = v;
+                }
+        }
+    }
+}
+
+// The workgroups' images added up: 8 f32x4 (128 bytes) of an image to a
+// workgroup, whose 32 sets of 8 threads share the images.
+template <int n>
+__global__ __launch_bounds__(256) void sum_images(const f32x4* images, int count, int L, int V, int cols, float beta,
+                                                  float* dweight, float* dbias) {
+    __shared__ f32x4 part[32][8];
+    const int each = V * L * n / 4, t = threadIdx.x, p = blockIdx.x * 8 + (t & 7);
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int b = t >> 3; b < count; b += 32) s += images[(int64_t)b * 2 * each + p];
+    part[t >> 3][t & 7] = s;
+    __syncthreads();
+    if (t >= 8) return;
+#pragma unroll
+    for (int g = 1; g < 32; ++g) s += part[g][t];
+    const int which = p / each, at = p % each;
+    const int lane = at % L, i = at / L / (n / 4), q = at / L % (n / 4);
+    const int c = (i * L + lane) * n;
+    const LastVec last = last_vec(cols, c, n);
+    float* out = which == 0 ? dweight : dbias;
+    if (out == nullptr) return;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (4 * q + e < last.skip) continue;
+        float* o = out + last.from + 4 * q + e;
+        *o = beta == 0.f ? s[e] : __builtin_fmaf(beta, *o, s[e]);
+    }
+}
+
+// Threads to a row and vectors to a thread of a width: 16 lanes up to 16
+// vectors, a wave up to 8 vectors a lane, then 2, 4 and 8 waves; 0 threads: no
+// such kernel (rows shorter than a vector, or longer than 4096 of them).
+struct Width {
+    int lanes, vecs;
+};
+inline Width width_of(int64_t cols, int n) {
+    if (cols < n || cols > 4096 * n) return Width{0, 0};
+    const int vecs = (int)((cols + n - 1) / n);
+    if (vecs <= 16) return Width{16, 1};
+    int lanes = 64;
+    while (vecs > lanes * 8) lanes *= 2;
+    return Width{lanes, (vecs + lanes - 1) / lanes};
+}
+
+constexpr int kImages = 256;        // workgroups of norm_grad: one to a compute unit
+
+template <typename T, int L, int V>
+hipError_t launch_fused(const NormGradArgs<T>& a, unsigned blocks, hipStream_t s) {
+    return a.R != nullptr ? launch_kernel(&norm_grad<T, L, V, true>, dim3(blocks), dim3(512), s, a)
+                          : launch_kernel(&norm_grad<T, L, V, false>, dim3(blocks), dim3(512), s, a);
+}
+
 template <typename T>
 hipError_t launch_grad(const NormGradArgs<T>& a, hipStream_t s) {
-    // The columns first: dX may take dY's place.
-    if (a.dweight != nullptr || a.dbias != nullptr) {
-        const hipError_t e = launch_kernel(&norm_grad_cols<T>, dim3(grid_for((a.cols + 63) / 64)), dim3(256), s, a);
-        if (e != hipSuccess) return e;
+    constexpr int n = Vec<T>::n;
+    const bool columns = a.dweight != nullptr || a.dbias != nullptr;
+    const Width w = width_of(a.cols, n);
+    if (w.lanes == 0 || a.rows == 0) {
+        // The columns first: dX may take dY's place.
+        if (columns) {
+            const hipError_t e = launch_kernel(&norm_grad_cols<T>, dim3(grid_for((a.cols + 63) / 64)), dim3(256), s, a);
+            if (e != hipSuccess) return e;
+        }
+        if (a.rows == 0) return hipSuccess;
+        return launch_kernel(&norm_grad_rows<T>, dim3(grid_for(a.rows)), dim3(256), s, a);
     }
-    if (a.rows == 0) return hipSuccess;
-    return launch_kernel(&norm_grad_rows<T>, dim3(grid_for(a.rows)), dim3(256), s, a);
+    const int groups = 512 / w.lanes;
+    const int64_t want = (a.rows + groups - 1) / groups;
+    const unsigned blocks = (unsigned)(want < kImages ? want : kImages);
+    hipError_t e = hipErrorInvalidConfiguration;
+    switch (w.lanes * 16 + w.vecs) {
+        case 16 * 16 + 1: e = launch_fused<T, 16, 1>(a, blocks, s); break;
+#define DG_WIDTH(L, V) case L * 16 + V: e = launch_fused<T, L, V>(a, blocks, s); break;
+        DG_WIDTH(64, 1) DG_WIDTH(64, 2) DG_WIDTH(64, 3) DG_WIDTH(64, 4)
+        DG_WIDTH(64, 5) DG_WIDTH(64, 6) DG_WIDTH(64, 7) DG_WIDTH(64, 8)
+        DG_WIDTH(128, 5) DG_WIDTH(128, 6) DG_WIDTH(128, 7) DG_WIDTH(128, 8)
+        DG_WIDTH(256, 5) DG_WIDTH(256, 6) DG_WIDTH(256, 7) DG_WIDTH(256, 8)
+        DG_WIDTH(512, 5) DG_WIDTH(512, 6) DG_WIDTH(512, 7) DG_WIDTH(512, 8)
+#undef DG_WIDTH
+    }
+    if (e != hipSuccess || !columns) return e;
+    const int each = w.vecs * w.lanes * n / 4;
+    return launch_kernel(&sum_images<n>, dim3((unsigned)(2 * each / 8)), dim3(256), s,
+                         reinterpret_cast<const f32x4*>(a.ws), (int)blocks, w.lanes, w.vecs, (int)a.cols, a.beta,
+                         a.dweight, a.dbias);
+}
+
+// An image is at most the columns rounded up to 8 x 512 values (bf16 at 512
+// lanes), twice, for each workgroup; sized alike for both types.
+size_t workspace(int64_t rows, int64_t cols) {
+    size_t most = 256;
+    for (int n : {Vec<uint16_t>::n, Vec<float>::n}) {
+        const Width w = width_of(cols, n);
+        if (w.lanes == 0) continue;
+        const int groups = 512 / w.lanes;
+        const int64_t want = (rows + groups - 1) / groups;
+        const size_t bytes = (size_t)(want < kImages ? want : kImages) * 2 * w.vecs * w.lanes * n * sizeof(float);
+        most = bytes > most ? bytes : most;
+    }
+    return most;
 }
 
 }  // namespace
 
-size_t layernorm_grad_workspace(int64_t, int64_t) { return 256; }
+size_t layernorm_grad_workspace(int64_t rows, int64_t cols) { return workspace(rows, cols); }
 
 hipError_t launch_layernorm(const NormArgs<uint16_t>& a, int, hipStream_t s) {
     return launch_kernel(&norm_rows<uint16_t>, dim3(grid_for(a.rows)), dim3(256), s, a);
