@@ -6,9 +6,14 @@
 // and the gradient of gates and loss in the logits.
 //
 // A token's logits lie in the registers of 16 lanes (64 above 256 experts), V
-// consecutive experts to a lane, so that a maximum is V - 1 operations and four
-// lane exchanges of the vector unit, for four tokens at once in a wave. The k
-// choices are k such searches; of equal logits the lowest lane's first takes it.
+// consecutive experts to a lane, four tokens at once in a wave. They are compared
+// as doubles that hold the logit and, in bits that fp32 leaves free, the
+// expert's number: these order like the logits, of equal ones the lower expert
+// first, and all differ, so that a maximum and a minimum are a comparator. Each
+// lane sorts its K largest (k rounded up to a power of two), and four exchanges
+// between lanes merge them: the larger of the first list's i-th and the second's
+// last-but-i-th are the K largest of both, and log2 K rounds of comparators sort
+// them. Lane j then holds choice j.
 //
 // The order of the rows needs every earlier token's choices. A workgroup takes 64
 // tokens at a time and marks each choice as a token's bit in its expert's 64-bit
@@ -32,23 +37,48 @@ constexpr int kChunk = 64;          // tokens at a time
 // One workgroup up to here.
 constexpr int kAlone = 256;
 
-__device__ __forceinline__ float max_of_16(float v) {
-    auto step = [](float a, auto ctrl) {
-        return fmaxf(a, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, a), ctrl(), 0xf, 0xf, true)));
-    };
-    v = step(v, [] { return 0xB1; });
-    v = step(v, [] { return 0x4E; });
-    v = step(v, [] { return 0x141; });
-    return step(v, [] { return 0x140; });
+typedef float f32x2_a4 __attribute__((ext_vector_type(2), aligned(4)));
+typedef uint32_t u32_a2 __attribute__((aligned(2)));
+typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
+
+// A value and that of the lane 16 or 32 lanes away: of both results, one is v
+// and the other the partner's, alike in both lanes.
+template <int APART>
+__device__ __forceinline__ void both_lanes(uint32_t v, uint32_t& x, uint32_t& y) {
+    if constexpr (APART == 16) {
+        const auto b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        x = b[0];
+        y = b[1];
+    } else {
+        const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        x = b[0];
+        y = b[1];
+    }
+}
+template <int APART>
+__device__ __forceinline__ float add_lanes(float v) {
+    uint32_t x, y;
+    both_lanes<APART>(__builtin_bit_cast(uint32_t, v), x, y);
+    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+template <int APART>
+__device__ __forceinline__ float max_lanes(float v) {
+    uint32_t x, y;
+    both_lanes<APART>(__builtin_bit_cast(uint32_t, v), x, y);
+    return fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+}
+
+template <int CTRL>
+__device__ __forceinline__ float max_dpp(float v) {
+    return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true)));
 }
 
 // Largest and sum over the L lanes of a row, in all of them.
 template <int L>
 __device__ __forceinline__ float row_max(float v) {
-    v = max_of_16(v);
+    v = max_dpp<0x140>(max_dpp<0x141>(max_dpp<0x4E>(max_dpp<0xB1>(v))));
     if constexpr (L == 64) {
-        v = fmaxf(v, __shfl_xor(v, 16, 64));
-        v = fmaxf(v, __shfl_xor(v, 32, 64));
+        v = max_lanes<32>(max_lanes<16>(v));
     }
     return v;
 }
@@ -57,41 +87,78 @@ __device__ __forceinline__ float row_sum(float v) {
     if constexpr (L == 64) return wave_sum(v);
     else return sum_of_16(v);
 }
-// The L lanes' bits of a ballot, lane 0's lowest.
-template <int L>
-__device__ __forceinline__ uint64_t row_ballot(bool b, int lane64) {
-    const uint64_t all = __ballot(b);
-    if constexpr (L == 64) return all;
-    else return (all >> (lane64 & 48)) & 0xffff;
-}
 
 // V logits of a row from expert e0 on: -infinity past the last. `whole`: the
 // experts are a multiple of V, and lanes lie inside or outside as a whole.
-template <typename T, int V>
-__device__ __forceinline__ void load_logits(const T* p, int e0, int experts, bool whole, float* l) {
-    T raw[V];
+template <int V>
+__device__ __forceinline__ void load_logits(const float* p, int e0, int experts, bool whole, float* l) {
     if (whole) {
-        __builtin_memcpy(raw, p + (e0 < experts ? e0 : 0), sizeof(raw));
+        p += e0 < experts ? e0 : 0;
+        if constexpr (V >= 4) {
+#pragma unroll
+            for (int q = 0; q < V / 4; ++q) {
+                const f32x4 w = *reinterpret_cast<const f32x4_a4*>(p + 4 * q);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) l[4 * q + i] = w[i];
+            }
+        } else if constexpr (V == 2) {
+            const f32x2_a4 w = *reinterpret_cast<const f32x2_a4*>(p);
+            l[0] = w[0];
+            l[1] = w[1];
+        } else {
+            l[0] = *p;
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) raw[i] = p[e0 + i < experts ? e0 + i : experts - 1];
+        for (int i = 0; i < V; ++i) l[i] = p[e0 + i < experts ? e0 + i : experts - 1];
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) l[i] = e0 + i < experts ? elem_f32(raw[i]) : -kInf;
+    for (int i = 0; i < V; ++i) l[i] = e0 + i < experts ? l[i] : -kInf;
+}
+template <int V>
+__device__ __forceinline__ void load_logits(const uint16_t* p, int e0, int experts, bool whole, float* l) {
+    constexpr int kWords = (V + 1) / 2;
+    uint32_t raw[kWords];
+    if (whole) {
+        p += e0 < experts ? e0 : 0;
+        if constexpr (V >= 8) {
+#pragma unroll
+            for (int q = 0; q < V / 8; ++q) {
+                const u32x4 w = *reinterpret_cast<const u32x4_a2*>(p + 8 * q);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) raw[4 * q + i] = w[i];
+            }
+        } else if constexpr (V == 4) {
+            const u32x2_a2 w = *reinterpret_cast<const u32x2_a2*>(p);
+            raw[0] = w[0];
+            raw[1] = w[1];
+        } else if constexpr (V == 2) {
+            raw[0] = *reinterpret_cast<const u32_a2*>(p);
+        } else {
+            raw[0] = *p;
+        }
+    } else {
+        uint16_t one[2 * kWords] = {};
+#pragma unroll
+        for (int i = 0; i < V; ++i) one[i] = p[e0 + i < experts ? e0 + i : experts - 1];
+#pragma unroll
+        for (int q = 0; q < kWords; ++q) raw[q] = one[2 * q] | (uint32_t)one[2 * q + 1] << 16;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const uint32_t w = raw[i / 2];
+        l[i] = e0 + i < experts ? __builtin_bit_cast(float, (i & 1) ? w & 0xffff0000u : w << 16) : -kInf;
+    }
 }
 
 // Softmax of a row: ex = exp(l - m) (0 for a row of -infinities), and 1 / their sum: 0 for
-// such a row, NaN for one that holds a NaN or +infinity.
+// such a row, NaN for one that holds a NaN or +infinity (whose difference from
+// itself is NaN).
 template <int L, int V>
-__device__ __forceinline__ float softmax(const float* l, float* ex, float& m, int lane64) {
-    bool bad = false;
-    float top = -kInf, s = 0.f;
+__device__ __forceinline__ float softmax(const float* l, float* ex, float& m) {
+    float top = l[0], s = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        bad |= !(l[i] < kInf);
-        top = fmaxf(top, l[i]);
-    }
-    bad = row_ballot<L>(bad, lane64) != 0;
+    for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
     top = row_max<L>(top);
     m = top == -kInf ? 0.f : top;
 #pragma unroll
@@ -100,7 +167,105 @@ __device__ __forceinline__ float softmax(const float* l, float* ex, float& m, in
         s += ex[i];
     }
     s = row_sum<L>(s);
-    return bad ? __builtin_nanf("") : (s > 0.f ? 1.f / s : 0.f);
+    return s == 0.f ? 0.f : 1.f / s;
+}
+
+// A logit and its expert as a double: the logit's 24 bits stay, and the lowest
+// ones take the expert so that the lower one is larger. -infinity becomes kNone, below
+// every other; a -0 counts as 0.
+constexpr double kNone = -0x1p1000;
+__device__ __forceinline__ double keyed(float l, int e) {
+    l += 0.f;
+    const uint64_t bits = __builtin_bit_cast(uint64_t, (double)l);
+    const uint32_t low = (uint32_t)(e ^ (kMaxExperts - 1)) ^ (uint32_t)((__builtin_bit_cast(int, l) >> 31) & (kMaxExperts - 1));
+    return l == -kInf ? kNone : __builtin_bit_cast(double, bits | low);
+}
+__device__ __forceinline__ int expert_of(double key) {
+    const u32x2 w = __builtin_bit_cast(u32x2, key);
+    return (int)((w[0] ^ (uint32_t)((int)~w[1] >> 31)) & (kMaxExperts - 1));
+}
+
+__device__ __forceinline__ void larger_first(double& a, double& b) {
+    const double big = __builtin_fmax(a, b);
+    b = __builtin_fmin(a, b);
+    a = big;
+}
+// v falls, or rises and falls: sorted, the largest first.
+template <int N>
+__device__ __forceinline__ void sort_bitonic(double* v) {
+#pragma unroll
+    for (int h = N / 2; h > 0; h /= 2)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if ((i & h) == 0) larger_first(v[i], v[i + h]);
+}
+template <int N>
+__device__ __forceinline__ void sort(double* v) {
+    if constexpr (N > 1) {
+        sort<N / 2>(v);
+        sort<N / 2>(v + N / 2);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) larger_first(v[i], v[N - 1 - i]);
+        sort_bitonic<N / 2>(v);
+        sort_bitonic<N / 2>(v + N / 2);
+    }
+}
+// The K largest of V keys, sorted.
+template <int V, int K>
+__device__ __forceinline__ void largest(double* v, double* out) {
+    if constexpr (V <= K) {
+        sort<V>(v);
+#pragma unroll
+        for (int i = 0; i < K; ++i) out[i] = i < V ? v[i < V ? i : 0] : kNone;
+    } else {
+        double other[K];
+        largest<V / 2, K>(v, out);
+        largest<V / 2, K>(v + V / 2, other);
+#pragma unroll
+        for (int i = 0; i < K; ++i) out[i] = __builtin_fmax(out[i], other[K - 1 - i]);
+        sort_bitonic<K>(out);
+    }
+}
+template <int K, int CTRL>
+__device__ __forceinline__ void merge_dpp(double* v) {
+    double o[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        const u32x2 w = __builtin_bit_cast(u32x2, v[i]);
+        o[i] = __builtin_bit_cast(double, u32x2{(uint32_t)__builtin_amdgcn_mov_dpp((int)w[0], CTRL, 0xf, 0xf, true),
+                                                (uint32_t)__builtin_amdgcn_mov_dpp((int)w[1], CTRL, 0xf, 0xf, true)});
+    }
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] = __builtin_fmax(v[i], o[K - 1 - i]);
+    sort_bitonic<K>(v);
+}
+template <int K, int APART>
+__device__ __forceinline__ void merge_lanes(double* v) {
+    double a[K], b[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        const u32x2 w = __builtin_bit_cast(u32x2, v[i]);
+        uint32_t alo, blo, ahi, bhi;
+        both_lanes<APART>(w[0], alo, blo);
+        both_lanes<APART>(w[1], ahi, bhi);
+        a[i] = __builtin_bit_cast(double, u32x2{alo, ahi});
+        b[i] = __builtin_bit_cast(double, u32x2{blo, bhi});
+    }
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] = __builtin_fmax(a[i], b[K - 1 - i]);
+    sort_bitonic<K>(v);
+}
+// Over the L lanes of a row: all of them end with the same K keys.
+template <int L, int K>
+__device__ __forceinline__ void merge_row(double* v) {
+    merge_dpp<K, 0xB1>(v);
+    merge_dpp<K, 0x4E>(v);
+    merge_dpp<K, 0x141>(v);
+    merge_dpp<K, 0x140>(v);
+    if constexpr (L == 64) {
+        merge_lanes<K, 16>(v);
+        merge_lanes<K, 32>(v);
+    }
 }
 
 // What choose leaves for place, for each workgroup: its counts (and its tokens
@@ -151,16 +316,14 @@ __device__ __forceinline__ void finish(const RouteArgs<T>& a, const int* counts,
 
 // Choices, gates and, into slots, each choice's place among its expert's rows of
 // this workgroup, whose tokens are `rows` from blockIdx.x * rows on (a multiple of
-// kChunk). ALONE: the only workgroup, which finishes too.
-template <typename T, int L, int V, bool ALONE>
-__global__ __launch_bounds__(kThreads) void choose(RouteArgs<T> a, Table table, int rows) {
+// kChunk). alone: the only workgroup, which finishes too.
+template <typename T, int L, int V, int K>
+__global__ __launch_bounds__(kThreads) void choose(RouteArgs<T> a, Table table, int rows, bool alone) {
     constexpr int kAtOnce = kThreads / L, kMost = L * V, kWaves = kThreads / 64;
     __shared__ unsigned long long bits[kMost];
-    __shared__ int chosen[kChunk * kMaxChoices];
-    __shared__ int total[kMost + 1];
-    __shared__ float sums[kWaves][kMost];
-    __shared__ int first[ALONE ? kMost + 1 : 1];
-    __shared__ float red[ALONE ? kWaves : 1];
+    __shared__ int chosen[kChunk * K];
+    __shared__ int total[kMost + 1], first[kMost + 1];
+    __shared__ float sums[kWaves][kMost], red[kWaves];
     const int t = threadIdx.x, lane64 = t & 63, lane = t % L, group = t / L;
     const int e0 = lane * V;
     const bool whole = a.experts % V == 0;
@@ -172,57 +335,44 @@ __global__ __launch_bounds__(kThreads) void choose(RouteArgs<T> a, Table table, 
     for (int64_t base = lo; base < hi; base += kChunk) {
         for (int e = t; e < a.experts; e += kThreads) bits[e] = 0;
         __syncthreads();
-#pragma unroll
+#pragma unroll 1
         for (int at = 0; at < kChunk; at += kAtOnce) {
             const int local = at + group;
             const int64_t token = base + local;
             const bool on = token < hi;
             float l[V], ex[V], m;
-            load_logits<T, V>(a.logits + (on ? token : hi - 1) * a.ldl, e0, a.experts, whole, l);
-            const float inv = softmax<L, V>(l, ex, m, lane64);
+            double key[V], top[K];
+            load_logits<V>(a.logits + (on ? token : hi - 1) * a.ldl, e0, a.experts, whole, l);
+            const float inv = softmax<L, V>(l, ex, m);
+#pragma unroll
+            for (int i = 0; i < V; ++i) psum[i] += ex[i] * (on ? inv : 0.f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) key[i] = keyed(l[i], e0 + i);
+            largest<V, K>(key, top);
+            merge_row<L, K>(top);
+            double mine = top[0];
+#pragma unroll
+            for (int j = 1; j < K; ++j) mine = lane == j ? top[j] : mine;
             const bool bad = !(inv == inv);
-            if (on) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) psum[i] += bad ? inv : ex[i] * inv;
-            }
-            float gate = bad ? inv : 0.f, sum = 0.f;
-            for (int j = 0; j < a.k; ++j) {
-                float mine = l[0];
-#pragma unroll
-                for (int i = 1; i < V; ++i) mine = fmaxf(mine, l[i]);
-                const float top = row_max<L>(mine);
-                const bool go = top > -kInf && !bad && on;
-                const int winner = __builtin_ctzll(row_ballot<L>(mine == top, lane64) | (1ull << 63));
-                const float p = __builtin_amdgcn_exp2f((top - m) * kLog2e);
-                if (go) {
-                    sum += p;
-                    if (lane == j) gate = p;
-                    if (lane == winner) {
-                        int e = -1;
-#pragma unroll
-                        for (int i = V - 1; i >= 0; --i) e = l[i] == top ? i : e;
-#pragma unroll
-                        for (int i = 0; i < V; ++i) l[i] = i == e ? -kInf : l[i];
-                        chosen[local * a.k + j] = e0 + e;
-                        atomicOr(&bits[e0 + e], 1ull << local);
-                    }
-                } else if (lane == 0) {
-                    chosen[local * a.k + j] = -1;
+            const bool go = on && !bad && lane < a.k && mine > kNone;
+            const int e = go ? expert_of(mine) : -1;
+            const float p = go ? __builtin_amdgcn_exp2f(((float)mine - m) * kLog2e) : 0.f;
+            const float sum = row_sum<L>(p);
+            if (lane < a.k) {
+                chosen[local * a.k + lane] = e;
+                if (go) atomicOr(&bits[e], 1ull << local);
+                if (on) {
+                    a.choice[token * a.k + lane] = e;
+                    a.gates[token * a.k + lane] = bad ? inv : (go ? (a.renormalize ? p / sum : p * inv) : 0.f);
                 }
-                if (j == 0 && go) some += 1;
             }
-            if (on && lane < a.k) {
-                if (!bad && sum > 0.f) gate = a.renormalize ? gate / sum : gate * inv;
-                a.gates[token * a.k + lane] = gate;
-            }
+            some += go && lane == 0;
         }
         __syncthreads();
         const int have = (int)(hi - base < kChunk ? hi - base : kChunk) * a.k;
         for (int i = t; i < have; i += kThreads) {
             const int e = chosen[i], local = i / a.k;
-            a.choice[base * a.k + i] = e;
-            a.slots[base * a.k + i] =
-                e < 0 ? -1 : total[e] + __builtin_popcountll(bits[e] & ((1ull << local) - 1));
+            a.slots[base * a.k + i] = e < 0 ? -1 : total[e] + __builtin_popcountll(bits[e] & ((1ull << local) - 1));
         }
         __syncthreads();
         for (int e = t; e < a.experts; e += kThreads) total[e] += __builtin_popcountll(bits[e]);
@@ -232,10 +382,7 @@ __global__ __launch_bounds__(kThreads) void choose(RouteArgs<T> a, Table table, 
     if (a.loss != nullptr) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if constexpr (L == 16) {
-                psum[i] += __shfl_xor(psum[i], 16, 64);
-                psum[i] += __shfl_xor(psum[i], 32, 64);
-            }
+            if constexpr (L == 16) psum[i] = add_lanes<32>(add_lanes<16>(psum[i]));
             if (lane64 < L) sums[t >> 6][e0 + i] = psum[i];
         }
     }
@@ -245,37 +392,51 @@ __global__ __launch_bounds__(kThreads) void choose(RouteArgs<T> a, Table table, 
             float s = sums[0][e];
 #pragma unroll
             for (int w = 1; w < kWaves; ++w) s += sums[w][e];
-            if constexpr (ALONE) sums[0][e] = s;
+            if (alone) sums[0][e] = s;
             else table.sums[(int64_t)blockIdx.x * a.experts + e] = s;
         }
-    if constexpr (!ALONE) {
+    if (!alone) {
         for (int e = t; e < table.stride; e += kThreads)
             table.counts[(int64_t)blockIdx.x * table.stride + e] = e <= a.experts ? (uint16_t)total[e] : 0;
-    } else {
-        if (t < 64) scan_counts(total, first, a.experts, t);
-        __syncthreads();
-        // The places were written by this workgroup; total is complete.
-        for (int64_t i = t; i < (int64_t)a.tokens * a.k; i += kThreads) {
-            const int e = a.choice[i];
-            if (e >= 0) a.slots[i] += first[e];
-        }
-        finish(a, total, first, sums[0], red);
+        return;
     }
+    if (t < 64) scan_counts(total, first, a.experts, t);
+    __syncthreads();
+    for (int64_t i = t; i < (int64_t)a.tokens * a.k; i += kThreads) {
+        const int e = a.choice[i];
+        if (e >= 0) a.slots[i] += first[e];
+    }
+    finish(a, total, first, sums[0], red);
 }
 
 // Slots, from each workgroup's counts: those of the workgroups before this one
-// and all of them. The first one writes offsets, counts and loss too.
+// and all of them. One workgroup more, the last, writes offsets, counts and loss.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void place(RouteArgs<T> a, Table table, int rows, int blocks) {
     __shared__ int before[kMaxExperts + 4], total[kMaxExperts + 4], first[kMaxExperts + 1];
-    __shared__ float sums[kMaxExperts], red[kThreads / 64];
+    __shared__ float part[kThreads], sums[kMaxExperts], red[kThreads / 64];
     const int t = threadIdx.x, words = table.stride / 4, sets = kThreads / words;
+    const bool last = (int)blockIdx.x == blocks;
+    const int64_t lo = (int64_t)blockIdx.x * rows * a.k, most = (int64_t)a.tokens * a.k;
+    const int64_t hi = last ? 0 : (lo + (int64_t)rows * a.k < most ? lo + (int64_t)rows * a.k : most);
+    // The first of this thread's choices, on its way while the counts are added.
+    int e0 = -1, s0 = 0;
+    if (lo + t < hi) {
+        e0 = a.choice[lo + t];
+        s0 = a.slots[lo + t];
+    }
+    // The last workgroup: a column of sums to a thread, 1024 / experts threads to a column.
+    const int share = kThreads / a.experts, set = t / a.experts;
+    float psum = 0.f;
+    if (last && a.loss != nullptr && set < share)
+#pragma unroll 8
+        for (int b = set; b < blocks; b += share) psum += table.sums[(int64_t)b * a.experts + t % a.experts];
     for (int e = t; e < table.stride; e += kThreads) before[e] = total[e] = 0;
     __syncthreads();
     if (t < words * sets) {
         const int w = t % words;
         int all[4] = {}, mine[4] = {};
-#pragma unroll 4
+#pragma unroll 8
         for (int b = t / words; b < blocks; b += sets) {
             const u32x2 v = *reinterpret_cast<const u32x2*>(table.counts + (int64_t)b * table.stride + 4 * w);
 #pragma unroll
@@ -291,34 +452,24 @@ __global__ __launch_bounds__(kThreads) void place(RouteArgs<T> a, Table table, i
             atomicAdd(&before[4 * w + i], mine[i]);
         }
     }
+    part[t] = psum;
     __syncthreads();
     if (t < 64) scan_counts(total, first, a.experts, t);
     __syncthreads();
-    const int64_t lo = (int64_t)blockIdx.x * rows * a.k, most = (int64_t)a.tokens * a.k;
-    const int64_t hi = lo + (int64_t)rows * a.k < most ? lo + (int64_t)rows * a.k : most;
-    for (int64_t i = lo + t; i < hi; i += kThreads) {
-        const int e = a.choice[i];
-        if (e >= 0) a.slots[i] += first[e] + before[e];
-    }
-    if (blockIdx.x != 0) return;
-    if (a.loss != nullptr) {
-        // A column of sums to each thread, 1024 / experts threads to a column: in a fixed order.
-        float* part = reinterpret_cast<float*>(before);
-        const int share = kThreads / a.experts, e = t % a.experts, s = t / a.experts;
-        float v = 0.f;
-        if (s < share)
-#pragma unroll 8
-            for (int b = s; b < blocks; b += share) v += table.sums[(int64_t)b * a.experts + e];
-        __syncthreads();
-        if (s < share) part[s * a.experts + e] = v;
-        __syncthreads();
-        for (int c = t; c < a.experts; c += kThreads) {
-            v = part[c];
-            for (int q = 1; q < share; ++q) v += part[q * a.experts + c];
-            sums[c] = v;
+    if (!last) {
+        if (e0 >= 0) a.slots[lo + t] = s0 + first[e0] + before[e0];
+        for (int64_t i = lo + t + kThreads; i < hi; i += kThreads) {
+            const int e = a.choice[i];
+            if (e >= 0) a.slots[i] += first[e] + before[e];
         }
-        __syncthreads();
+        return;
     }
+    for (int c = t; c < a.experts; c += kThreads) {
+        float v = part[c];
+        for (int q = 1; q < share; ++q) v += part[q * a.experts + c];
+        sums[c] = v;
+    }
+    __syncthreads();
     finish(a, total, first, sums, red);
 }
 
@@ -331,7 +482,7 @@ __global__ __launch_bounds__(256) void route_grad(RouteGradArgs<T> a) {
         int in;
     };
     __shared__ Chosen lds[256 * V];
-    const int t = threadIdx.x, lane64 = t & 63, lane = t % L, e0 = lane * V;
+    const int t = threadIdx.x, lane = t % L, e0 = lane * V;
     Chosen* row = lds + t / L * (L * V);
     const bool whole = a.experts % V == 0;
     float bal[V], all = 0.f;
@@ -350,7 +501,7 @@ __global__ __launch_bounds__(256) void route_grad(RouteGradArgs<T> a) {
         const bool on = token < a.tokens;
         const int64_t from = on ? token : a.tokens - 1;
         float l[V], p[V], g[V], m;
-        load_logits<T, V>(a.logits + from * a.ldl, e0, a.experts, whole, l);
+        load_logits<V>(a.logits + from * a.ldl, e0, a.experts, whole, l);
         int e = -1;
         float d = 0.f;
         if (a.dgates != nullptr && lane < a.k) {
@@ -362,7 +513,7 @@ __global__ __launch_bounds__(256) void route_grad(RouteGradArgs<T> a) {
         __syncthreads();
         if (e >= 0 && e < a.experts) row[e] = Chosen{d, 1};
         __syncthreads();
-        const float inv = softmax<L, V>(l, p, m, lane64);
+        const float inv = softmax<L, V>(l, p, m);
         float s = 0.f, sd = 0.f, sum = 0.f;
         Chosen c[V];
 #pragma unroll
@@ -415,16 +566,23 @@ int rows_each(int tokens) {
 int64_t blocks_of(int tokens) { return ((int64_t)tokens + rows_each(tokens) - 1) / rows_each(tokens); }
 size_t sums_at(int64_t blocks, int experts) { return ((size_t)blocks * table_stride(experts) * 2 + 255) & ~(size_t)255; }
 
-template <typename T, int L, int V>
+template <typename T, int L, int V, int K>
 hipError_t launch_choose(const RouteArgs<T>& a, const Table& table, hipStream_t s) {
     if (a.tokens <= kAlone)
-        return launch_kernel(&choose<T, L, V, true>, dim3(1), dim3(kThreads), s, a, table,
-                             (a.tokens + kChunk - 1) / kChunk * kChunk);
+        return launch_kernel(&choose<T, L, V, K>, dim3(1), dim3(kThreads), s, a, table,
+                             (a.tokens + kChunk - 1) / kChunk * kChunk, true);
     const int rows = rows_each(a.tokens);
     const unsigned blocks = (unsigned)blocks_of(a.tokens);
-    const hipError_t e = launch_kernel(&choose<T, L, V, false>, dim3(blocks), dim3(kThreads), s, a, table, rows);
+    const hipError_t e = launch_kernel(&choose<T, L, V, K>, dim3(blocks), dim3(kThreads), s, a, table, rows, false);
     if (e != hipSuccess) return e;
-    return launch_kernel(&place<T>, dim3(blocks), dim3(kThreads), s, a, table, rows, (int)blocks);
+    return launch_kernel(&place<T>, dim3(blocks + 1), dim3(kThreads), s, a, table, rows, (int)blocks);
+}
+template <typename T, int L, int V>
+hipError_t launch_choose(const RouteArgs<T>& a, const Table& table, hipStream_t s) {
+    if (a.k <= 2) return launch_choose<T, L, V, 2>(a, table, s);
+    if (a.k <= 4) return launch_choose<T, L, V, 4>(a, table, s);
+    if (a.k <= 8) return launch_choose<T, L, V, 8>(a, table, s);
+    return launch_choose<T, L, V, 16>(a, table, s);
 }
 
 template <typename T>
