@@ -68,6 +68,85 @@ __global__ __launch_bounds__(256) void norm_rows(NormArgs<T> a) {
     }
 }
 
+// L threads to a row (16, or whole waves), V vectors to a thread: one read of X, whose
+// values stay in registers between the mean, the squares and Y.
+template <typename T, int L, int V>
+__global__ __launch_bounds__(L < 256 ? 256 : L) void norm(NormArgs<T> a) {
+    constexpr int n = Vec<T>::n, kThreads = L < 256 ? 256 : L, kGroups = kThreads / L, kWaves = L / 64;
+    __shared__ float part[2][kThreads / 64];
+    const int t = threadIdx.x, lane = t % L, cols = (int)a.cols;
+    const int64_t row0 = (int64_t)blockIdx.x * kGroups + t / L;
+    const bool on = row0 < a.rows;                      // kWaves <= 4 rows share no barrier that some skip
+    const int64_t row = on ? row0 : a.rows - 1;
+    int col[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) col[i] = (i * L + lane) * n;
+    const LastVec last = last_vec(cols, col[V - 1], n);
+    col[V - 1] = last.from;
+    Vec<T> x[V], w[V], b[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i].load(a.X + row * a.ldx + col[i], n);
+    if (a.weight != nullptr) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[i].load(a.weight + col[i], n);
+    }
+    if (a.bias != nullptr) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) b[i].load(a.bias + col[i], n);
+    }
+    const auto row_sum = [&](float v, int turn) {
+        if constexpr (L == 16) return sum_of_16(v);
+        v = wave_sum(v);
+        if constexpr (kWaves > 1) {
+            if ((t & 63) == 0) part[turn][t >> 6] = v;
+            __syncthreads();
+            v = 0.f;
+#pragma unroll
+            for (int q = 0; q < kWaves; ++q) v += part[turn][t / L * kWaves + q];
+        }
+        return v;
+    };
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int e = 0; e < n; ++e) s += i == V - 1 && e < last.skip ? 0.f : x[i].at(e);
+    const float m = row_sum(s, 0) / (float)cols;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int e = 0; e < n; ++e) {
+            const float d = x[i].at(e) - m;
+            s = i == V - 1 && e < last.skip ? s : __builtin_fmaf(d, d, s);
+        }
+    const float r = 1.f / sqrtf(row_sum(s, 1) / (float)cols + a.eps);
+    if (!on) return;
+    if (lane == 0) {
+        if (a.mean != nullptr) a.mean[row] = m;
+        if (a.rstd != nullptr) a.rstd[row] = r;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float y[n];
+#pragma unroll
+        for (int e = 0; e < n; ++e) {
+            y[e] = (x[i].at(e) - m) * r;
+            if (a.weight != nullptr) y[e] *= w[i].at(e);
+            if (a.bias != nullptr) y[e] += b[i].at(e);
+        }
+        x[i].set(y);
+        T* p = a.Y + row * a.ldy + col[i];
+        if (i < V - 1 || last.skip == 0) {
+            x[i].store(p, n);
+        } else {
+#pragma unroll
+            for (int e = 0; e < n; ++e)
+                if (e >= last.skip) x[i].store1(p + e, e);
+        }
+    }
+}
+
 // dX: one workgroup to a row, read twice.
 template <typename T>
 __global__ __launch_bounds__(256) void norm_grad_rows(NormGradArgs<T> a) {
@@ -335,6 +414,7 @@ inline Width width_of(int64_t cols, int n) {
     return Width{lanes, (vecs + lanes - 1) / lanes};
 }
 
+constexpr int64_t kMaxNormRows = 1 << 22, kManyRows = 1024;
 constexpr int kImages = 256;        // workgroups of norm_grad: one to a compute unit
 
 template <typename T, int L, int V>
@@ -393,16 +473,46 @@ size_t workspace(int64_t rows, int64_t cols) {
     return most;
 }
 
+template <typename T, int L, int V>
+hipError_t launch_rows(const NormArgs<T>& a, hipStream_t s) {
+    constexpr int kThreads = L < 256 ? 256 : L, kGroups = kThreads / L;
+    return launch_kernel(&norm<T, L, V>, dim3((unsigned)((a.rows + kGroups - 1) / kGroups)), dim3(kThreads), s, a);
+}
+template <typename T, int L>
+hipError_t launch_rows(const NormArgs<T>& a, int vecs, hipStream_t s) {
+    switch ((vecs + L - 1) / L) {
+        case 1: return launch_rows<T, L, 1>(a, s);
+        case 2: return launch_rows<T, L, 2>(a, s);
+        case 3: return launch_rows<T, L, 3>(a, s);
+        case 4: return launch_rows<T, L, 4>(a, s);
+        case 5: return launch_rows<T, L, 5>(a, s);
+        case 6: return launch_rows<T, L, 6>(a, s);
+        case 7: return launch_rows<T, L, 7>(a, s);
+        case 8: return launch_rows<T, L, 8>(a, s);
+    }
+    return hipErrorInvalidConfiguration;
+}
+
+template <typename T>
+hipError_t launch_norm(const NormArgs<T>& a, hipStream_t s) {
+    constexpr int n = Vec<T>::n;
+    const int64_t vecs = (a.cols + n - 1) / n;
+    if (a.cols < n || vecs > 8 * 1024 || a.rows > kMaxNormRows)
+        return launch_kernel(&norm_rows<T>, dim3(grid_for(a.rows)), dim3(256), s, a);
+    if (vecs <= 16) return launch_rows<T, 16, 1>(a, s);
+    // A wave to a row where the rows fill the card, more lanes where they don't.
+    const int v = (int)vecs, most = a.rows >= kManyRows ? 8 : 1;
+    if (v <= 64 * most) return launch_rows<T, 64>(a, v, s);
+    if (v <= 256 * most) return launch_rows<T, 256>(a, v, s);
+    return launch_rows<T, 1024>(a, v, s);
+}
+
 }  // namespace
 
 size_t layernorm_grad_workspace(int64_t rows, int64_t cols) { return workspace(rows, cols); }
 
-hipError_t launch_layernorm(const NormArgs<uint16_t>& a, int, hipStream_t s) {
-    return launch_kernel(&norm_rows<uint16_t>, dim3(grid_for(a.rows)), dim3(256), s, a);
-}
-hipError_t launch_layernorm(const NormArgs<float>& a, int, hipStream_t s) {
-    return launch_kernel(&norm_rows<float>, dim3(grid_for(a.rows)), dim3(256), s, a);
-}
+hipError_t launch_layernorm(const NormArgs<uint16_t>& a, int, hipStream_t s) { return launch_norm(a, s); }
+hipError_t launch_layernorm(const NormArgs<float>& a, int, hipStream_t s) { return launch_norm(a, s); }
 hipError_t launch_layernorm_grad(const NormGradArgs<uint16_t>& a, hipStream_t s) { return launch_grad(a, s); }
 hipError_t launch_layernorm_grad(const NormGradArgs<float>& a, hipStream_t s) { return launch_grad(a, s); }
 

@@ -499,8 +499,8 @@ gemm_status_t gemm_bf16_grouped_wgrad_f32(int64_t groups, int64_t M, int64_t N, 
  *
  * weight, bias: cols values of X's type, or NULL for 1 and 0. mean, rstd: rows
  * fp32 values each, which receive m and r for the gradient, or NULL. Y may be X.
- * eps >= 0 (finite); a constant row with eps == 0 has r = infinity, and NaN in
- * Y. A row that holds an infinity or a NaN gets NaN. The mean is taken first and the squares of
+ * eps >= 0 (finite); with eps == 0 a constant row divides by zero, or by the
+ * rounding of its mean. A row that holds an infinity or a NaN gets NaN. The mean is taken first and the squares of
  * the differences from it then, so rows far from zero lose nothing. rows == 0 or
  * cols == 0 does nothing. */
 gemm_status_t gemm_layernorm_bf16(int64_t rows, int64_t cols, float eps, const uint16_t* X, int64_t ldx,
