@@ -208,6 +208,26 @@ __device__ __forceinline__ float wave_sum(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
+// A value and that of the lane 16 or 32 lanes away: of both results, one is v
+// and the other the partner's, alike in both lanes.
+template <int APART>
+__device__ __forceinline__ void both_lanes(uint32_t v, uint32_t& x, uint32_t& y) {
+    if constexpr (APART == 16) {
+        const auto b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        x = b[0];
+        y = b[1];
+    } else {
+        const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        x = b[0];
+        y = b[1];
+    }
+}
+template <int APART>
+__device__ __forceinline__ float add_lanes(float v) {
+    uint32_t x, y;
+    both_lanes<APART>(__builtin_bit_cast(uint32_t, v), x, y);
+    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
 // Workgroups for `units` independent pieces: as many, up to what a grid
 // dimension takes; the kernels stride over the rest.
 inline unsigned grid_for(int64_t units) {

@@ -216,25 +216,48 @@ __global__ __launch_bounds__(256) void norm_grad_cols(NormGradArgs<T> a) {
 // Both at once, in one pass over X and dY: L threads to a row (16, or whole
 // waves), V vectors to a thread, which keeps the row's values in registers
 // between the row's sums and dX, and its columns' sums of dY h and dY in 2 V n
-// more. A workgroup of 512 threads takes 512 / L rows at a time and adds its
-// threads' column sums up in LDS at the end, into one image of the registers
-// for each workgroup; sum_images adds those, in their order.
-template <typename T, int L, int V, bool RES>
+// more. PRE: the next row is on its way meanwhile. A workgroup of 512 threads takes
+// 512 / L rows at a time and adds its threads' column sums up in LDS at the end,
+// into one image of the registers for each workgroup; sum_images adds those.
+template <typename T, int V, bool RES>
+struct RowOf {
+    Vec<T> x[V], dy[V], res[RES ? V : 1];
+    float r, m;
+    __device__ __forceinline__ void load(const NormGradArgs<T>& a, int64_t row, const int* col) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            x[i].load(a.X + row * a.ldx + col[i], Vec<T>::n);
+            dy[i].load(a.dY + row * a.lddy + col[i], Vec<T>::n);
+            if constexpr (RES) res[i].load(a.R + row * a.ldr + col[i], Vec<T>::n);
+        }
+        r = a.rstd[row];
+        m = a.mean[row];
+    }
+};
+
+template <typename T, int L, int V, bool RES, bool PRE>
 __global__ __launch_bounds__(512, 2) void norm_grad(NormGradArgs<T> a) {
     constexpr int n = Vec<T>::n, kGroups = 512 / L, kWaves = L / 64;
+    constexpr int kSets = L == 16 ? 8 : kGroups;                // of column sums, after the lanes of a wave have met
     constexpr int kImage = V * L * n / 4;                       // f32x4 of one sum
     __shared__ union {
         u32x4 w[V * L];
-        f32x4 image[kImage];
+        f32x4 image[kSets > 1 ? kSets / 2 : 1][kSets > 1 ? 2 * kImage : 1];
     } lds;
     __shared__ float part[2][8][2];
-    const int t = threadIdx.x, lane = t % L, group = t / L, wave = t >> 6;
+    // Uniform in a wave, and kept in scalar registers, where a row has whole waves.
+    const int t = threadIdx.x, lane = t % L, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int group = L == 16 ? t / L : wave / (kWaves > 0 ? kWaves : 1);
     const int cols = (int)a.cols;
     int col[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) col[i] = (i * L + lane) * n;
     const LastVec last = last_vec(cols, col[V - 1], n);
     col[V - 1] = last.from;
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    int64_t row0 = (int64_t)blockIdx.x * kGroups, row = row0 + group;
+    RowOf<T, V, RES> now;
+    if (PRE && row < a.rows) now.load(a, row, col);
     if (group == 0) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -250,41 +273,32 @@ __global__ __launch_bounds__(512, 2) void norm_grad(NormGradArgs<T> a) {
             lds.w[i * L + lane] = __builtin_bit_cast(u32x4, w.w);
         }
     }
-    __syncthreads();
+    lds_only_barrier();
     float dw[V][n] = {}, db[V][n] = {};
     const float inv = 1.f / (float)cols;
     int turn = 0;
-    for (int64_t row0 = (int64_t)blockIdx.x * kGroups; row0 < a.rows; row0 += (int64_t)gridDim.x * kGroups, turn ^= 1) {
-        const int64_t row = row0 + group;
-        const bool on = row < a.rows;
-        Vec<T> x[V], dy[V], res[V];
-        float r = 0.f, mr = 0.f, sg = 0.f, sgh = 0.f;
+    // One row in each group, or (`on`) in some: the waves of a row meet in it.
+    // Every lane stores whole vectors: where the last ones of a row overlap, they
+    // hold the same bits. With that a turn's loads and stores are the same in
+    // number on every path, and the wait for a row's loads leaves the
+    // stores before and the loads after them in flight.
+    const auto one = [&](bool on) {
+        float sg = 0.f, sgh = 0.f;
         if (on) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                x[i].load(a.X + row * a.ldx + col[i], n);
-                dy[i].load(a.dY + row * a.lddy + col[i], n);
-            }
-            if constexpr (RES) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) res[i].load(a.R + row * a.ldr + col[i], n);
-            }
-            r = a.rstd[row];
-            mr = -a.mean[row];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 Vec<T> w;
                 w.w = __builtin_bit_cast(decltype(w.w), lds.w[i * L + lane]);
 #pragma unroll
                 for (int e = 0; e < n; ++e) {
-                    const float h = (x[i].at(e) + mr) * r;
-                    float d = dy[i].at(e);
-                    if (i == V - 1) d = e >= last.skip ? d : 0.f;
+                    const bool skip = i == V - 1 && e < last.skip;
+                    const float h = (now.x[i].at(e) - now.m) * now.r;
+                    const float d = skip ? 0.f : now.dy[i].at(e);
                     const float g = d * w.at(e);
                     sg += g;
-                    sgh = i == V - 1 && e < last.skip ? sgh : __builtin_fmaf(g, h, sgh);
+                    sgh = skip ? sgh : __builtin_fmaf(g, h, sgh);
                     db[i][e] += d;
-                    dw[i][e] = i == V - 1 && e < last.skip ? 0.f : __builtin_fmaf(d, h, dw[i][e]);
+                    dw[i][e] = skip ? 0.f : __builtin_fmaf(d, h, dw[i][e]);
                 }
             }
         }
@@ -299,7 +313,7 @@ __global__ __launch_bounds__(512, 2) void norm_grad(NormGradArgs<T> a) {
                     part[turn][wave][0] = sg;
                     part[turn][wave][1] = sgh;
                 }
-                __syncthreads();
+                lds_only_barrier();
                 sg = sgh = 0.f;
 #pragma unroll
                 for (int w = 0; w < kWaves; ++w) {
@@ -308,87 +322,101 @@ __global__ __launch_bounds__(512, 2) void norm_grad(NormGradArgs<T> a) {
                 }
             }
         }
-        if (!on) continue;
+        turn ^= 1;
+        if (!on) return;
         const float c1 = sg * inv, c2 = sgh * inv;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
+            // Unpacked again: the values of the first pass would take registers that spill.
+            asm volatile("" : "+v"(now.x[i].w), "+v"(now.dy[i].w));
             Vec<T> w;
             w.w = __builtin_bit_cast(decltype(w.w), lds.w[i * L + lane]);
             float out[n];
 #pragma unroll
             for (int e = 0; e < n; ++e) {
-                const float h = (x[i].at(e) + mr) * r;
-                const float in = __builtin_fmaf(-h, c2, __builtin_fmaf(dy[i].at(e), w.at(e), -c1));
-                out[e] = __builtin_fmaf(r, in, RES ? res[i].at(e) : 0.f);
+                const float h = (now.x[i].at(e) - now.m) * now.r;
+                const float in = __builtin_fmaf(-h, c2, __builtin_fmaf(now.dy[i].at(e), w.at(e), -c1));
+                out[e] = __builtin_fmaf(now.r, in, RES ? now.res[RES ? i : 0].at(e) : 0.f);
             }
-            x[i].set(out);
-            T* p = a.dX + row * a.lddx + col[i];
-            if (i < V - 1 || last.skip == 0) {
-                x[i].store(p, n);
-            } else {
-#pragma unroll
-                for (int e = 0; e < n; ++e)
-                    if (e >= last.skip) x[i].store1(p + e, e);
-            }
+            w.set(out);
+            w.store(a.dX + row * a.lddx + col[i], n);
         }
+    };
+    for (; row0 + kGroups <= a.rows; row0 += step, row += step) {
+        RowOf<T, V, RES> next;
+        if constexpr (PRE) next.load(a, row + step < a.rows ? row + step : row, col);
+        else now.load(a, row, col);
+        one(true);
+        if constexpr (PRE) now = next;
+    }
+    if (row0 < a.rows) {
+        const bool on = row < a.rows;
+        if (!PRE && on) now.load(a, row, col);
+        one(on);
     }
     if (a.dweight == nullptr && a.dbias == nullptr) return;
-    // Rows of 16 lanes first: their sums meet within the wave.
-    constexpr int kSets = L == 16 ? 8 : kGroups;
+    // The sets of column sums meet two by two.
     const int set = L == 16 ? wave : group;
     if constexpr (L == 16) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int e = 0; e < n; ++e) {
-                dw[i][e] += __shfl_xor(dw[i][e], 16, 64);
-                dw[i][e] += __shfl_xor(dw[i][e], 32, 64);
-                db[i][e] += __shfl_xor(db[i][e], 16, 64);
-                db[i][e] += __shfl_xor(db[i][e], 32, 64);
+                dw[i][e] = add_lanes<32>(add_lanes<16>(dw[i][e]));
+                db[i][e] = add_lanes<32>(add_lanes<16>(db[i][e]));
             }
     }
     const bool mine = L != 16 || (t & 63) < 16;
+    const auto each = [&](auto&& f) {
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        f32x4* image = reinterpret_cast<f32x4*>(a.ws) + ((int64_t)blockIdx.x * 2 + which) * kImage;
-        for (int s = 0; s < kSets; ++s) {
-            if (kSets > 1) __syncthreads();
-            if (set != s || !mine) continue;
+        for (int i = 0; i < V; ++i)
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+            for (int q = 0; q < n / 4; ++q) {
+                const int at = (i * (n / 4) + q) * L + lane;
+                f(at, &dw[i][4 * q]);
+                f(kImage + at, &db[i][4 * q]);
+            }
+    };
 #pragma unroll
-                for (int q = 0; q < n / 4; ++q) {
-                    const int at = (i * (n / 4) + q) * L + lane;
-                    f32x4 v;
+    for (int half = kSets / 2; half > 0; half /= 2) {
+        lds_only_barrier();
+        if (set >= half && set < 2 * half && mine)
+            each([&](int at, const float* v) { lds.image[set - half][at] = f32x4{v[0], v[1], v[2], v[3]}; });
+        lds_only_barrier();
+        if (set < half && mine)
+            each([&](int at, float* v) {
+                const f32x4 o = lds.image[set][at];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = which == 0 ? dw[i][4 * q + e] : db[i][4 * q + e];
-                    if (s > 0) v += lds.image[at];
-                    if (s < kSets - 1) lds.image[at] = v;
-                    else image[at] = v;
-                }
-        }
+                for (int e = 0; e < 4; ++e) v[e] += o[e];
+            });
     }
+    f32x4* image = reinterpret_cast<f32x4*>(a.ws) + (int64_t)blockIdx.x * 2 * kImage;
+    if (set == 0 && mine) each([&](int at, const float* v) { image[at] = f32x4{v[0], v[1], v[2], v[3]}; });
 }
 
-// The workgroups' images added up: 8 f32x4 (128 bytes) of an image to a
-// workgroup, whose 32 sets of 8 threads share the images.
+// The workgroups' images added up: 4 f32x4 of an image to a workgroup, whose 64
+// sets of 4 threads share the images.
 template <int n>
 __global__ __launch_bounds__(256) void sum_images(const f32x4* images, int count, int L, int V, int cols, float beta,
                                                   float* dweight, float* dbias) {
-    __shared__ f32x4 part[32][8];
-    const int each = V * L * n / 4, t = threadIdx.x, p = blockIdx.x * 8 + (t & 7);
+    __shared__ f32x4 part[64][4];
+    const int each = V * L * n / 4, t = threadIdx.x, p = blockIdx.x * 4 + (t & 3);
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int b = t >> 3; b < count; b += 32) s += images[(int64_t)b * 2 * each + p];
-    part[t >> 3][t & 7] = s;
+#pragma unroll 4
+    for (int b = t >> 2; b < count; b += 64) s += images[(int64_t)b * 2 * each + p];
+    part[t >> 2][t & 3] = s;
     __syncthreads();
-    if (t >= 8) return;
+    if (t >= 32) return;
 #pragma unroll
-    for (int g = 1; g < 32; ++g) s += part[g][t];
+    for (int g = 1; g < 8; ++g) s += part[(t >> 2) + 8 * g][t & 3];
+    part[t >> 2][t & 3] = s;
+    __builtin_amdgcn_wave_barrier();
+    if (t >= 4) return;
+#pragma unroll
+    for (int g = 1; g < 8; ++g) s += part[g][t];
     const int which = p / each, at = p % each;
     const int lane = at % L, i = at / L / (n / 4), q = at / L % (n / 4);
-    const int c = (i * L + lane) * n;
-    const LastVec last = last_vec(cols, c, n);
+    const LastVec last = last_vec(cols, (i * L + lane) * n, n);
     float* out = which == 0 ? dweight : dbias;
     if (out == nullptr) return;
 #pragma unroll
@@ -399,28 +427,40 @@ __global__ __launch_bounds__(256) void sum_images(const f32x4* images, int count
     }
 }
 
-// Threads to a row and vectors to a thread of a width: 16 lanes up to 16
-// vectors, a wave up to 8 vectors a lane, then 2, 4 and 8 waves; 0 threads: no
-// such kernel (rows shorter than a vector, or longer than 4096 of them).
+// Threads to a row and vectors to a thread: 16 lanes up to 16 vectors; then as few
+// waves as hold the row in 32 values a thread; up to 64 in 8 waves. 0 threads: no such
+// kernel (rows shorter than a vector, or longer than 32768 values in bf16, 16384 in fp32).
 struct Width {
     int lanes, vecs;
 };
 inline Width width_of(int64_t cols, int n) {
-    if (cols < n || cols > 4096 * n) return Width{0, 0};
-    const int vecs = (int)((cols + n - 1) / n);
+    const int64_t vecs = (cols + n - 1) / n;
+    if (cols < n || vecs > 512 * 8) return Width{0, 0};
     if (vecs <= 16) return Width{16, 1};
     int lanes = 64;
-    while (vecs > lanes * 8) lanes *= 2;
-    return Width{lanes, (vecs + lanes - 1) / lanes};
+    while (lanes < 512 && vecs * n > lanes * 32) lanes *= 2;
+    return Width{lanes, (int)((vecs + lanes - 1) / lanes)};
 }
 
-constexpr int64_t kMaxNormRows = 1 << 22, kManyRows = 1024;
+constexpr int64_t kManyRows = 1024;
 constexpr int kImages = 256;        // workgroups of norm_grad: one to a compute unit
 
 template <typename T, int L, int V>
 hipError_t launch_fused(const NormGradArgs<T>& a, unsigned blocks, hipStream_t s) {
-    return a.R != nullptr ? launch_kernel(&norm_grad<T, L, V, true>, dim3(blocks), dim3(512), s, a)
-                          : launch_kernel(&norm_grad<T, L, V, false>, dim3(blocks), dim3(512), s, a);
+    // Two rows (8 or, with R, 12 registers a vector) and the column sums fit 256
+    // registers beside the rest.
+    constexpr int kSums = 2 * V * Vec<T>::n;
+    constexpr bool kPre = kSums <= 64, kPreRes = kPre && 24 * V + kSums <= 200;
+    return a.R != nullptr ? launch_kernel(&norm_grad<T, L, V, true, kPreRes>, dim3(blocks), dim3(512), s, a)
+                          : launch_kernel(&norm_grad<T, L, V, false, kPre>, dim3(blocks), dim3(512), s, a);
+}
+// The widths that width_of gives for L lanes: above a half of 32 values a thread
+// (from one vector on with a single wave), with 8 waves up to 64.
+template <typename T, int L, int V = L == 64 ? 1 : 16 / Vec<T>::n + 1>
+hipError_t launch_fused(const NormGradArgs<T>& a, int vecs, unsigned blocks, hipStream_t s) {
+    if (vecs == V) return launch_fused<T, L, V>(a, blocks, s);
+    if constexpr (V < (L == 512 ? 8 : 32 / Vec<T>::n)) return launch_fused<T, L, V + 1>(a, vecs, blocks, s);
+    return hipErrorInvalidConfiguration;
 }
 
 template <typename T>
@@ -441,19 +481,14 @@ hipError_t launch_grad(const NormGradArgs<T>& a, hipStream_t s) {
     const int64_t want = (a.rows + groups - 1) / groups;
     const unsigned blocks = (unsigned)(want < kImages ? want : kImages);
     hipError_t e = hipErrorInvalidConfiguration;
-    switch (w.lanes * 16 + w.vecs) {
-        case 16 * 16 + 1: e = launch_fused<T, 16, 1>(a, blocks, s); break;
-#define DG_WIDTH(L, V) case L * 16 + V: e = launch_fused<T, L, V>(a, blocks, s); break;
-        DG_WIDTH(64, 1) DG_WIDTH(64, 2) DG_WIDTH(64, 3) DG_WIDTH(64, 4)
-        DG_WIDTH(64, 5) DG_WIDTH(64, 6) DG_WIDTH(64, 7) DG_WIDTH(64, 8)
-        DG_WIDTH(128, 5) DG_WIDTH(128, 6) DG_WIDTH(128, 7) DG_WIDTH(128, 8)
-        DG_WIDTH(256, 5) DG_WIDTH(256, 6) DG_WIDTH(256, 7) DG_WIDTH(256, 8)
-        DG_WIDTH(512, 5) DG_WIDTH(512, 6) DG_WIDTH(512, 7) DG_WIDTH(512, 8)
-#undef DG_WIDTH
-    }
+    if (w.lanes == 16) e = launch_fused<T, 16, 1>(a, blocks, s);
+    if (w.lanes == 64) e = launch_fused<T, 64>(a, w.vecs, blocks, s);
+    if (w.lanes == 128) e = launch_fused<T, 128>(a, w.vecs, blocks, s);
+    if (w.lanes == 256) e = launch_fused<T, 256>(a, w.vecs, blocks, s);
+    if (w.lanes == 512) e = launch_fused<T, 512>(a, w.vecs, blocks, s);
     if (e != hipSuccess || !columns) return e;
     const int each = w.vecs * w.lanes * n / 4;
-    return launch_kernel(&sum_images<n>, dim3((unsigned)(2 * each / 8)), dim3(256), s,
+    return launch_kernel(&sum_images<n>, dim3((unsigned)(2 * each / 4)), dim3(256), s,
                          reinterpret_cast<const f32x4*>(a.ws), (int)blocks, w.lanes, w.vecs, (int)a.cols, a.beta,
                          a.dweight, a.dbias);
 }
@@ -473,10 +508,16 @@ size_t workspace(int64_t rows, int64_t cols) {
     return most;
 }
 
+template <typename T>
+hipError_t launch_general(const NormArgs<T>& a, hipStream_t s) {
+    return launch_kernel(&norm_rows<T>, dim3(grid_for(a.rows)), dim3(256), s, a);
+}
 template <typename T, int L, int V>
 hipError_t launch_rows(const NormArgs<T>& a, hipStream_t s) {
     constexpr int kThreads = L < 256 ? 256 : L, kGroups = kThreads / L;
-    return launch_kernel(&norm<T, L, V>, dim3((unsigned)((a.rows + kGroups - 1) / kGroups)), dim3(kThreads), s, a);
+    const int64_t blocks = (a.rows + kGroups - 1) / kGroups;
+    if (blocks * kThreads > INT32_MAX) return launch_general(a, s);       // past what a launch takes
+    return launch_kernel(&norm<T, L, V>, dim3((unsigned)blocks), dim3(kThreads), s, a);
 }
 template <typename T, int L>
 hipError_t launch_rows(const NormArgs<T>& a, int vecs, hipStream_t s) {
@@ -497,8 +538,7 @@ template <typename T>
 hipError_t launch_norm(const NormArgs<T>& a, hipStream_t s) {
     constexpr int n = Vec<T>::n;
     const int64_t vecs = (a.cols + n - 1) / n;
-    if (a.cols < n || vecs > 8 * 1024 || a.rows > kMaxNormRows)
-        return launch_kernel(&norm_rows<T>, dim3(grid_for(a.rows)), dim3(256), s, a);
+    if (a.cols < n || vecs > 8 * 1024) return launch_general(a, s);
     if (vecs <= 16) return launch_rows<T, 16, 1>(a, s);
     // A wave to a row where the rows fill the card, more lanes where they don't.
     const int v = (int)vecs, most = a.rows >= kManyRows ? 8 : 1;

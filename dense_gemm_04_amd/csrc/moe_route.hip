@@ -41,26 +41,6 @@ typedef float f32x2_a4 __attribute__((ext_vector_type(2), aligned(4)));
 typedef uint32_t u32_a2 __attribute__((aligned(2)));
 typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
 
-// A value and that of the lane 16 or 32 lanes away: of both results, one is v
-// and the other the partner's, alike in both lanes.
-template <int APART>
-__device__ __forceinline__ void both_lanes(uint32_t v, uint32_t& x, uint32_t& y) {
-    if constexpr (APART == 16) {
-        const auto b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-        x = b[0];
-        y = b[1];
-    } else {
-        const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-        x = b[0];
-        y = b[1];
-    }
-}
-template <int APART>
-__device__ __forceinline__ float add_lanes(float v) {
-    uint32_t x, y;
-    both_lanes<APART>(__builtin_bit_cast(uint32_t, v), x, y);
-    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
-}
 template <int APART>
 __device__ __forceinline__ float max_lanes(float v) {
     uint32_t x, y;
