@@ -5,6 +5,10 @@
 //     gather    Y(slot_tj) = X(t)
 //     combine   C(t) = R(t) + sum_j gate_tj Y(slot_tj)
 //     gradient  dY(slot_tj) = gate_tj dC(t),  dgate_tj = dC(t) . Y(slot_tj)
+//
+// Bound by memory. A token's k slots are read first and held in scalar registers
+// (K: k rounded up to a power of two), so that the k rows' loads leave
+// together.
 
 #include "layer.hpp"
 
@@ -12,87 +16,157 @@ namespace dg {
 namespace {
 
 constexpr int kVec = Vec<uint16_t>::n;
+constexpr int kColumns = 256 * kVec;             // of a workgroup at a time
 
-__global__ __launch_bounds__(256) void gather(RowsArgs a) {
-    for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x)
-        for (int64_t c = (int64_t)threadIdx.x * kVec; c < a.cols; c += 256 * kVec) {
-            const int valid = inside(a.cols, c, kVec);
-            Vec<uint16_t> x;
-            x.load(a.X + t * a.ldx + c, valid);
-            for (int j = 0; j < a.k; ++j) {
-                const int64_t slot = a.slots[t * a.k + j];
-                if (slot >= 0 && slot < a.rows) x.store(a.out + slot * a.ldo + c, valid);
-            }
+// A token's slots as scalars: -1 where absent, outside the rows or past k.
+template <int K>
+__device__ __forceinline__ void load_slots(const RowsArgs& a, int64_t t, int* slot) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) slot[j] = a.slots[t * a.k + (j < a.k ? j : 0)];
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        slot[j] = __builtin_amdgcn_readfirstlane(slot[j]);
+        if (j >= a.k || slot[j] < 0 || slot[j] >= a.rows) slot[j] = -1;
+    }
+}
+template <int K>
+__device__ __forceinline__ void load_gates(const RowsArgs& a, int64_t t, float* gate) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) gate[j] = j >= a.k ? 0.f : (a.gates != nullptr ? a.gates[t * a.k + j] : 1.f);
+}
+
+template <int K>
+__device__ __forceinline__ void gather_one(const RowsArgs& a, int64_t t, int64_t c) {
+    const int valid = inside(a.cols, c, kVec);
+    Vec<uint16_t> x;
+    x.load(a.X + t * a.ldx + (valid > 0 ? c : 0), valid);
+    int slot[K];
+    load_slots<K>(a, t, slot);
+    if (valid == 0) return;
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+        if (slot[j] >= 0) x.store(a.out + slot[j] * a.ldo + c, valid);
+}
+
+template <int K>
+__device__ __forceinline__ void combine_one(const RowsArgs& a, int64_t t, int64_t c) {
+    const int valid = inside(a.cols, c, kVec);
+    int slot[K];
+    float gate[K];
+    load_slots<K>(a, t, slot);
+    load_gates<K>(a, t, gate);
+    if (valid == 0) return;
+    Vec<uint16_t> y[K], r;
+    float sum[kVec] = {};
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        y[j].w = u32x4{0, 0, 0, 0};
+        if (slot[j] >= 0) y[j].load(a.Y + slot[j] * a.ldy + c, valid);
+    }
+    if (a.X != nullptr) r.load(a.X + t * a.ldx + c, valid);
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        if (j >= a.k) break;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) sum[e] = __builtin_fmaf(gate[j], y[j].at(e), sum[e]);
+    }
+    if (a.X != nullptr) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) sum[e] += r.at(e);
+    }
+    r.set(sum);
+    r.store(a.out + t * a.ldo + c, valid);
+}
+
+// A workgroup takes kColumns columns of a token (tokens over grid.y; both
+// strides are for sizes past the grid).
+template <int K, bool COMBINE>
+__global__ __launch_bounds__(256) void rows(RowsArgs a) {
+    for (int64_t t = blockIdx.y; t < a.tokens; t += gridDim.y)
+        for (int64_t c0 = (int64_t)blockIdx.x * kColumns; c0 < a.cols; c0 += (int64_t)gridDim.x * kColumns) {
+            if constexpr (COMBINE) combine_one<K>(a, t, c0 + threadIdx.x * kVec);
+            else gather_one<K>(a, t, c0 + threadIdx.x * kVec);
         }
 }
 
-__global__ __launch_bounds__(256) void combine(RowsArgs a) {
-    for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x)
-        for (int64_t c = (int64_t)threadIdx.x * kVec; c < a.cols; c += 256 * kVec) {
-            const int valid = inside(a.cols, c, kVec);
-            Vec<uint16_t> v;
-            float sum[kVec] = {};
-            for (int j = 0; j < a.k; ++j) {
-                const int64_t slot = a.slots[t * a.k + j];
-                const bool there = slot >= 0 && slot < a.rows;
-                const float gate = a.gates != nullptr ? a.gates[t * a.k + j] : 1.f;
-                v.load(there ? a.Y + slot * a.ldy + c : a.Y, there ? valid : 0);
+// A token's gradients, by a workgroup: the products with all its rows are sums
+// over the whole row. part: LDS that the token before did not use.
+template <int K>
+__device__ __forceinline__ void combine_grad_one(const RowsArgs& a, int64_t t, float (*part)[K]) {
+    int slot[K];
+    float gate[K], dot[K] = {};
+    load_slots<K>(a, t, slot);
+    load_gates<K>(a, t, gate);
+    for (int64_t c = threadIdx.x * kVec; c < a.cols; c += kColumns) {
+        const int valid = inside(a.cols, c, kVec);
+        Vec<uint16_t> dc, y[K];
+        dc.load(a.X + t * a.ldx + c, valid);
+        if (a.dgates != nullptr) {
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) sum[e] = __builtin_fmaf(gate, v.at(e), sum[e]);
+            for (int j = 0; j < K; ++j) {
+                y[j].w = u32x4{0, 0, 0, 0};
+                if (slot[j] >= 0) y[j].load(a.Y + slot[j] * a.ldy + c, valid);
             }
-            if (a.X != nullptr) {
-                v.load(a.X + t * a.ldx + c, valid);
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) sum[e] += v.at(e);
-            }
-            v.set(sum);
-            v.store(a.out + t * a.ldo + c, valid);
         }
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            if (slot[j] < 0) continue;
+            float dy[kVec];
+            if (a.dgates != nullptr) {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) dot[j] = __builtin_fmaf(dc.at(e), y[j].at(e), dot[j]);
+            }
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) dy[e] = gate[j] * dc.at(e);
+            y[j].set(dy);
+            y[j].store(a.out + slot[j] * a.ldo + c, valid);
+        }
+    }
+    if (a.dgates == nullptr) return;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        const float s = wave_sum(dot[j]);
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6][j] = s;
+    }
+    lds_only_barrier();
+    const int j = threadIdx.x;
+    if (j < a.k) a.dgates[t * a.k + j] = (part[0][j] + part[1][j]) + (part[2][j] + part[3][j]);
 }
 
+template <int K>
 __global__ __launch_bounds__(256) void combine_grad(RowsArgs a) {
-    __shared__ float part[4];
-    for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x)
-        for (int j = 0; j < a.k; ++j) {
-            const int64_t slot = a.slots[t * a.k + j];
-            const bool there = slot >= 0 && slot < a.rows;
-            const float gate = a.gates != nullptr ? a.gates[t * a.k + j] : 1.f;
-            float dot = 0.f;
-            if (there)
-                for (int64_t c = (int64_t)threadIdx.x * kVec; c < a.cols; c += 256 * kVec) {
-                    const int valid = inside(a.cols, c, kVec);
-                    Vec<uint16_t> dc, y;
-                    float dy[kVec];
-                    dc.load(a.X + t * a.ldx + c, valid);
-                    if (a.dgates != nullptr) {
-                        y.load(a.Y + slot * a.ldy + c, valid);
-#pragma unroll
-                        for (int e = 0; e < kVec; ++e) dot = __builtin_fmaf(dc.at(e), y.at(e), dot);
-                    }
-#pragma unroll
-                    for (int e = 0; e < kVec; ++e) dy[e] = gate * dc.at(e);
-                    y.set(dy);
-                    y.store(a.out + slot * a.ldo + c, valid);
-                }
-            if (a.dgates == nullptr) continue;
-            dot = wave_sum(dot);
-            __syncthreads();
-            if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
-            __syncthreads();
-            if (threadIdx.x == 0) a.dgates[t * a.k + j] = (part[0] + part[1]) + (part[2] + part[3]);
-        }
+    __shared__ float part[2][4][K];
+    int turn = 0;
+    for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x, turn ^= 1) combine_grad_one<K>(a, t, part[turn]);
+}
+
+// K: k rounded up to a power of two.
+template <typename F>
+hipError_t with_choices(int k, F&& launch) {
+    if (k == 1) return launch(std::integral_constant<int, 1>{});
+    if (k == 2) return launch(std::integral_constant<int, 2>{});
+    if (k <= 4) return launch(std::integral_constant<int, 4>{});
+    if (k <= 8) return launch(std::integral_constant<int, 8>{});
+    return launch(std::integral_constant<int, 16>{});
+}
+
+dim3 rows_grid(const RowsArgs& a) {
+    const int64_t chunks = (a.cols + kColumns - 1) / kColumns;
+    return dim3((unsigned)(chunks < 64 ? chunks : 64), (unsigned)(a.tokens < 65535 ? a.tokens : 65535));
 }
 
 }  // namespace
 
 hipError_t launch_gather(const RowsArgs& a, hipStream_t s) {
-    return launch_kernel(&gather, dim3(grid_for(a.tokens)), dim3(256), s, a);
+    return with_choices(a.k, [&](auto k) { return launch_kernel(&rows<k(), false>, rows_grid(a), dim3(256), s, a); });
 }
 hipError_t launch_combine(const RowsArgs& a, hipStream_t s) {
-    return launch_kernel(&combine, dim3(grid_for(a.tokens)), dim3(256), s, a);
+    return with_choices(a.k, [&](auto k) { return launch_kernel(&rows<k(), true>, rows_grid(a), dim3(256), s, a); });
 }
 hipError_t launch_combine_grad(const RowsArgs& a, hipStream_t s) {
-    return launch_kernel(&combine_grad, dim3(grid_for(a.tokens)), dim3(256), s, a);
+    return with_choices(a.k, [&](auto k) {
+        return launch_kernel(&combine_grad<k()>, dim3(grid_for(a.tokens)), dim3(256), s, a);
+    });
 }
 
 }  // namespace dg
