@@ -31,11 +31,16 @@ namespace {
 
 constexpr float kInf = __builtin_inff();
 constexpr float kLog2e = 1.44269504f;
-constexpr int kThreads = 1024;      // of choose and place
+// Of choose: two turns for 64 tokens of 16 lanes. With 1024 threads the waves' share
+// of setting up and adding up counts twice (16384 x 128, 8 choices 9.8 us against
+// 8.7, x 256 14.3 against 11.5).
+constexpr int kThreads = 512;
 constexpr int kChunk = 64;          // tokens at a time
 
-// One workgroup up to here.
-constexpr int kAlone = 256;
+// One workgroup up to here: 64 tokens at a time take as long as two launches at two
+// turns (128 tokens x 128 experts, 8 choices 12.2 us against 7.7 + 4.6 and a
+// second call; 256 x 64, 4 choices 12.6 against 5.2 + 5.4).
+constexpr int kAlone = 128;
 
 typedef float f32x2_a4 __attribute__((ext_vector_type(2), aligned(4)));
 typedef uint32_t u32_a2 __attribute__((aligned(2)));
@@ -252,7 +257,7 @@ __device__ __forceinline__ void merge_row(double* v) {
 // with a choice at [experts]) and its sums of p.
 struct Table {
     uint16_t* counts;       // workgroups x stride
-    float* sums;            // workgroups x experts
+    float* sums;            // workgroups x stride
     int stride;
 };
 inline __host__ __device__ int table_stride(int experts) { return (experts + 1 + 3) & ~3; }
@@ -273,23 +278,23 @@ __device__ __forceinline__ void scan_counts(const int* counts, int* first, int e
 
 // Offsets, counts and loss from the counts and sums of p over all tokens, by one
 // workgroup; `red` has a float for each of its waves.
-template <typename T>
+template <int THREADS, typename T>
 __device__ __forceinline__ void finish(const RouteArgs<T>& a, const int* counts, const int* first, const float* sums,
                                        float* red) {
     const int t = threadIdx.x;
-    for (int e = t; e <= a.experts; e += kThreads) {
+    for (int e = t; e <= a.experts; e += THREADS) {
         a.offsets[e] = first[e];
         a.counts[e] = counts[e];
     }
     if (a.loss == nullptr) return;
     float s = 0.f;
-    for (int e = t; e < a.experts; e += kThreads) s += (float)counts[e] * sums[e];
+    for (int e = t; e < a.experts; e += THREADS) s += (float)counts[e] * sums[e];
     s = wave_sum(s);
     if ((t & 63) == 0) red[t >> 6] = s;
     __syncthreads();
     if (t != 0) return;
     s = 0.f;
-    for (int w = 0; w < kThreads / 64; ++w) s += red[w];
+    for (int w = 0; w < THREADS / 64; ++w) s += red[w];
     const int all = first[a.experts], tokens = counts[a.experts];
     *a.loss = (float)a.experts * (s / (float)(all > 1 ? all : 1)) / (float)(tokens > 1 ? tokens : 1);
 }
@@ -373,7 +378,7 @@ __global__ __launch_bounds__(kThreads) void choose(RouteArgs<T> a, Table table, 
 #pragma unroll
             for (int w = 1; w < kWaves; ++w) s += sums[w][e];
             if (alone) sums[0][e] = s;
-            else table.sums[(int64_t)blockIdx.x * a.experts + e] = s;
+            else table.sums[(int64_t)blockIdx.x * table.stride + e] = s;
         }
     if (!alone) {
         for (int e = t; e < table.stride; e += kThreads)
@@ -386,16 +391,21 @@ __global__ __launch_bounds__(kThreads) void choose(RouteArgs<T> a, Table table, 
         const int e = a.choice[i];
         if (e >= 0) a.slots[i] += first[e];
     }
-    finish(a, total, first, sums[0], red);
+    finish<kThreads>(a, total, first, sums[0], red);
 }
 
 // Slots, from each workgroup's counts: those of the workgroups before this one
 // and all of them. One workgroup more, the last, writes offsets, counts and loss.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void place(RouteArgs<T> a, Table table, int rows, int blocks) {
+// The tables are read by up to kSets sets of threads, 4 columns to a thread; a
+// column's sets are added by one thread. N threads: 512, or 1024 above 128 experts
+// (16384 tokens x 128 experts 7.7 us with 512, 8.1 with 1024; x 256 12.7 and 11.0).
+constexpr int kSets = 32;
+template <typename T, int N>
+__global__ __launch_bounds__(N) void place(RouteArgs<T> a, Table table, int rows, int blocks) {
     __shared__ int before[kMaxExperts + 4], total[kMaxExperts + 4], first[kMaxExperts + 1];
-    __shared__ float part[kThreads], sums[kMaxExperts], red[kThreads / 64];
-    const int t = threadIdx.x, words = table.stride / 4, sets = kThreads / words;
+    __shared__ float sums[kMaxExperts], red[N / 64];
+    __shared__ u32x4 part[2][N];
+    const int t = threadIdx.x, words = table.stride / 4, sets = N / words < kSets ? N / words : kSets;
     const bool last = (int)blockIdx.x == blocks;
     const int64_t lo = (int64_t)blockIdx.x * rows * a.k, most = (int64_t)a.tokens * a.k;
     const int64_t hi = last ? 0 : (lo + (int64_t)rows * a.k < most ? lo + (int64_t)rows * a.k : most);
@@ -405,52 +415,65 @@ __global__ __launch_bounds__(kThreads) void place(RouteArgs<T> a, Table table, i
         e0 = a.choice[lo + t];
         s0 = a.slots[lo + t];
     }
-    // The last workgroup: a column of sums to a thread, 1024 / experts threads to a column.
-    const int share = kThreads / a.experts, set = t / a.experts;
-    float psum = 0.f;
-    if (last && a.loss != nullptr && set < share)
-#pragma unroll 8
-        for (int b = set; b < blocks; b += share) psum += table.sums[(int64_t)b * a.experts + t % a.experts];
-    for (int e = t; e < table.stride; e += kThreads) before[e] = total[e] = 0;
-    __syncthreads();
+    // Two 16-bit counts to an addition, for as many rows as cannot overflow them: the
+    // vector unit, not memory, is what every workgroup's sum of the whole table
+    // costs.
     if (t < words * sets) {
-        const int w = t % words;
-        int all[4] = {}, mine[4] = {};
+        const int w = t % words, at_once = 65535 / rows * sets;
+        u32x4 all = {0, 0, 0, 0}, mine = {0, 0, 0, 0};
+        for (int b0 = t / words; b0 < blocks; b0 += at_once) {
+            const int end = blocks - b0 < at_once ? blocks : b0 + at_once;
+            u32x2 va = {0, 0}, vm = {0, 0};
 #pragma unroll 8
-        for (int b = t / words; b < blocks; b += sets) {
-            const u32x2 v = *reinterpret_cast<const u32x2*>(table.counts + (int64_t)b * table.stride + 4 * w);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = (int)((i & 1) ? v[i >> 1] >> 16 : v[i >> 1] & 0xffffu);
-                all[i] += n;
-                mine[i] += b < (int)blockIdx.x ? n : 0;
+            for (int b = b0; b < end; b += sets) {
+                const u32x2 v = *reinterpret_cast<const u32x2*>(table.counts + (int64_t)b * table.stride + 4 * w);
+                const bool earlier = b < (int)blockIdx.x;
+                va += v;
+                vm += u32x2{earlier ? v[0] : 0u, earlier ? v[1] : 0u};
             }
+            all += u32x4{va[0] & 0xffffu, va[0] >> 16, va[1] & 0xffffu, va[1] >> 16};
+            mine += u32x4{vm[0] & 0xffffu, vm[0] >> 16, vm[1] & 0xffffu, vm[1] >> 16};
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            atomicAdd(&total[4 * w + i], all[i]);
-            atomicAdd(&before[4 * w + i], mine[i]);
-        }
+        part[0][t] = all;
+        part[1][t] = mine;
     }
-    part[t] = psum;
+    f32x4 psum = {0.f, 0.f, 0.f, 0.f};
+    if (last && a.loss != nullptr && t < words * sets) {
+#pragma unroll 8
+        for (int b = t / words; b < blocks; b += sets)
+            psum += *reinterpret_cast<const f32x4*>(table.sums + (int64_t)b * table.stride + 4 * (t % words));
+    }
+    __syncthreads();
+    for (int e = t; e < table.stride; e += N) {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(part) + e;
+        int all = 0, mine = 0;
+        for (int q = 0; q < sets; ++q) {
+            all += (int)p[q * table.stride];
+            mine += (int)p[4 * N + q * table.stride];
+        }
+        total[e] = all;
+        before[e] = mine;
+    }
     __syncthreads();
     if (t < 64) scan_counts(total, first, a.experts, t);
+    if (last && t < words * sets) part[0][t] = __builtin_bit_cast(u32x4, psum);
     __syncthreads();
     if (!last) {
         if (e0 >= 0) a.slots[lo + t] = s0 + first[e0] + before[e0];
-        for (int64_t i = lo + t + kThreads; i < hi; i += kThreads) {
+        for (int64_t i = lo + t + N; i < hi; i += N) {
             const int e = a.choice[i];
             if (e >= 0) a.slots[i] += first[e] + before[e];
         }
         return;
     }
-    for (int c = t; c < a.experts; c += kThreads) {
-        float v = part[c];
-        for (int q = 1; q < share; ++q) v += part[q * a.experts + c];
-        sums[c] = v;
+    for (int e = t; e < a.experts; e += N) {
+        const float* p = reinterpret_cast<const float*>(part[0]) + e;
+        float v = p[0];
+        for (int q = 1; q < sets; ++q) v += p[q * table.stride];
+        sums[e] = v;
     }
     __syncthreads();
-    finish(a, total, first, sums, red);
+    finish<N>(a, total, first, sums, red);
 }
 
 // The gradient, L lanes to a token. The choices' gradients reach the lanes that
@@ -536,9 +559,10 @@ __global__ __launch_bounds__(256) void route_grad(RouteGradArgs<T> a) {
 }
 
 // Tokens to a workgroup: 64, or as many more that the workgroups stay at most
-// 1024 (each adds up all their counts), within 16 bits for a count.
+// 256, one to a compute unit (each adds up all their counts), within 16 bits
+// for a count.
 int rows_each(int tokens) {
-    constexpr int64_t kBlocks = 1024, kMostRows = 65472;
+    constexpr int64_t kBlocks = 256, kMostRows = 65472;
     const int64_t chunks = ((int64_t)tokens + kChunk * kBlocks - 1) / (kChunk * kBlocks);
     const int64_t rows = (chunks < 1 ? 1 : chunks) * kChunk;
     return (int)(rows < kMostRows ? rows : kMostRows);
@@ -555,7 +579,9 @@ hipError_t launch_choose(const RouteArgs<T>& a, const Table& table, hipStream_t 
     const unsigned blocks = (unsigned)blocks_of(a.tokens);
     const hipError_t e = launch_kernel(&choose<T, L, V, K>, dim3(blocks), dim3(kThreads), s, a, table, rows, false);
     if (e != hipSuccess) return e;
-    return launch_kernel(&place<T>, dim3(blocks + 1), dim3(kThreads), s, a, table, rows, (int)blocks);
+    if (a.experts > 128)
+        return launch_kernel(&place<T, 1024>, dim3(blocks + 1), dim3(1024), s, a, table, rows, (int)blocks);
+    return launch_kernel(&place<T, 512>, dim3(blocks + 1), dim3(512), s, a, table, rows, (int)blocks);
 }
 template <typename T, int L, int V>
 hipError_t launch_choose(const RouteArgs<T>& a, const Table& table, hipStream_t s) {
@@ -597,7 +623,7 @@ hipError_t launch_grad(const RouteGradArgs<T>& a, hipStream_t s) {
 
 size_t route_workspace(int64_t tokens, int64_t experts, int) {
     const int64_t blocks = blocks_of((int)tokens);
-    return sums_at(blocks, (int)experts) + (size_t)blocks * experts * sizeof(float) + 256;
+    return sums_at(blocks, (int)experts) + (size_t)blocks * table_stride((int)experts) * sizeof(float) + 256;
 }
 
 hipError_t launch_route(const RouteArgs<uint16_t>& a, hipStream_t s) { return launch(a, s); }
