@@ -699,6 +699,8 @@ def moe_combine_grad(dC, slots, dY, Y=None, gates=None, dgates=None, stream=None
     k = _slots_of(slots, T)
     _want("dY", dY, bf16, 2, (None, cols))
     if dgates is not None:
+        if Y is None:
+            raise ValueError("dgates need Y")
         _want("Y", Y, bf16, 2, (dY.shape[0], cols))
         _flat("dgates", dgates, (torch.float32,), (T, k))
     if gates is not None:

@@ -696,7 +696,7 @@ gemm_status_t layernorm(int64_t rows, int64_t cols, float eps, const T* X, int64
     if (rows == 0 || cols == 0) return GEMM_OK;
     if (X == nullptr || Y == nullptr) return GEMM_ERR_INVALID_VALUE;
     const dg::NormArgs<T> a{rows, cols, eps, X, ldx, weight, bias, Y, ldy, mean, rstd};
-    return on_device([&](int cus) { return dg::launch_layernorm(a, cus, reinterpret_cast<hipStream_t>(stream)); });
+    return on_device([&](int) { return dg::launch_layernorm(a, reinterpret_cast<hipStream_t>(stream)); });
 }
 
 template <typename T>

@@ -21,8 +21,8 @@ struct NormArgs {
     float* mean;                    // or null
     float* rstd;                    // or null
 };
-hipError_t launch_layernorm(const NormArgs<uint16_t>& a, int cus, hipStream_t s);
-hipError_t launch_layernorm(const NormArgs<float>& a, int cus, hipStream_t s);
+hipError_t launch_layernorm(const NormArgs<uint16_t>& a, hipStream_t s);
+hipError_t launch_layernorm(const NormArgs<float>& a, hipStream_t s);
 
 template <typename T>
 struct NormGradArgs {

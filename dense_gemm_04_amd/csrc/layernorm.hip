@@ -187,6 +187,10 @@ __global__ __launch_bounds__(256) void norm_grad_rows(NormGradArgs<T> a) {
     }
 }
 
+__device__ __forceinline__ void add_to(float* out, float beta, float v) {
+    *out = beta == 0.f ? v : __builtin_fmaf(beta, *out, v);
+}
+
 // dweight and dbias: 64 columns to a workgroup, whose 4 waves share the rows.
 template <typename T>
 __global__ __launch_bounds__(256) void norm_grad_cols(NormGradArgs<T> a) {
@@ -208,8 +212,8 @@ __global__ __launch_bounds__(256) void norm_grad_cols(NormGradArgs<T> a) {
         if (wave != 0 || c >= a.cols) continue;
         dw = (part[0][0][lane] + part[0][1][lane]) + (part[0][2][lane] + part[0][3][lane]);
         db = (part[1][0][lane] + part[1][1][lane]) + (part[1][2][lane] + part[1][3][lane]);
-        if (a.dweight != nullptr) a.dweight[c] = a.beta == 0.f ? dw : __builtin_fmaf(a.beta, a.dweight[c], dw);
-        if (a.dbias != nullptr) a.dbias[c] = a.beta == 0.f ? db : __builtin_fmaf(a.beta, a.dbias[c], db);
+        if (a.dweight != nullptr) add_to(a.dweight + c, a.beta, dw);
+        if (a.dbias != nullptr) add_to(a.dbias + c, a.beta, db);
     }
 }
 
@@ -390,8 +394,38 @@ __global__ __launch_bounds__(512, 2) void norm_grad(NormGradArgs<T> a) {
                 for (int e = 0; e < 4; ++e) v[e] += o[e];
             });
     }
-    f32x4* image = reinterpret_cast<f32x4*>(a.ws) + (int64_t)blockIdx.x * 2 * kImage;
-    if (set == 0 && mine) each([&](int at, const float* v) { image[at] = f32x4{v[0], v[1], v[2], v[3]}; });
+    if (set != 0 || !mine) return;
+    if (gridDim.x > 1) {
+        f32x4* image = reinterpret_cast<f32x4*>(a.ws) + (int64_t)blockIdx.x * 2 * kImage;
+        each([&](int at, const float* v) { image[at] = f32x4{v[0], v[1], v[2], v[3]}; });
+        return;
+    }
+    // The only workgroup.
+    const auto out = [&](float* to, const float* v, int i) {
+        if (to == nullptr) return;
+#pragma unroll
+        for (int q = 0; q < n / 4; ++q) {
+            float* p = to + col[i] + 4 * q;
+            if (i < V - 1 || last.skip == 0) {
+                f32x4 w = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+                if (a.beta != 0.f) {
+                    const f32x4 o = *reinterpret_cast<const f32x4_a4*>(p);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = __builtin_fmaf(a.beta, o[e], w[e]);
+                }
+                *reinterpret_cast<f32x4_a4*>(p) = w;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (4 * q + e >= last.skip) add_to(p + e, a.beta, v[4 * q + e]);
+            }
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        out(a.dweight, dw[i], i);
+        out(a.dbias, db[i], i);
+    }
 }
 
 // The workgroups' images added up: 4 f32x4 of an image to a workgroup, whose 64
@@ -422,8 +456,7 @@ __global__ __launch_bounds__(256) void sum_images(const f32x4* images, int count
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         if (4 * q + e < last.skip) continue;
-        float* o = out + last.from + 4 * q + e;
-        *o = beta == 0.f ? s[e] : __builtin_fmaf(beta, *o, s[e]);
+        add_to(out + last.from + 4 * q + e, beta, s[e]);
     }
 }
 
@@ -444,6 +477,13 @@ inline Width width_of(int64_t cols, int n) {
 
 constexpr int64_t kManyRows = 1024;
 constexpr int kImages = 256;        // workgroups of norm_grad: one to a compute unit
+// One alone up to two turns: a second launch costs as much as the second turn.
+inline int64_t grad_blocks(int64_t rows, const Width& w) {
+    const int groups = 512 / w.lanes;
+    if (rows <= 2 * groups) return 1;
+    const int64_t want = (rows + groups - 1) / groups;
+    return want < kImages ? want : kImages;
+}
 
 template <typename T, int L, int V>
 hipError_t launch_fused(const NormGradArgs<T>& a, unsigned blocks, hipStream_t s) {
@@ -477,16 +517,14 @@ hipError_t launch_grad(const NormGradArgs<T>& a, hipStream_t s) {
         if (a.rows == 0) return hipSuccess;
         return launch_kernel(&norm_grad_rows<T>, dim3(grid_for(a.rows)), dim3(256), s, a);
     }
-    const int groups = 512 / w.lanes;
-    const int64_t want = (a.rows + groups - 1) / groups;
-    const unsigned blocks = (unsigned)(want < kImages ? want : kImages);
+    const unsigned blocks = (unsigned)grad_blocks(a.rows, w);
     hipError_t e = hipErrorInvalidConfiguration;
     if (w.lanes == 16) e = launch_fused<T, 16, 1>(a, blocks, s);
     if (w.lanes == 64) e = launch_fused<T, 64>(a, w.vecs, blocks, s);
     if (w.lanes == 128) e = launch_fused<T, 128>(a, w.vecs, blocks, s);
     if (w.lanes == 256) e = launch_fused<T, 256>(a, w.vecs, blocks, s);
     if (w.lanes == 512) e = launch_fused<T, 512>(a, w.vecs, blocks, s);
-    if (e != hipSuccess || !columns) return e;
+    if (e != hipSuccess || !columns || blocks == 1) return e;
     const int each = w.vecs * w.lanes * n / 4;
     return launch_kernel(&sum_images<n>, dim3((unsigned)(2 * each / 4)), dim3(256), s,
                          reinterpret_cast<const f32x4*>(a.ws), (int)blocks, w.lanes, w.vecs, (int)a.cols, a.beta,
@@ -500,9 +538,7 @@ size_t workspace(int64_t rows, int64_t cols) {
     for (int n : {Vec<uint16_t>::n, Vec<float>::n}) {
         const Width w = width_of(cols, n);
         if (w.lanes == 0) continue;
-        const int groups = 512 / w.lanes;
-        const int64_t want = (rows + groups - 1) / groups;
-        const size_t bytes = (size_t)(want < kImages ? want : kImages) * 2 * w.vecs * w.lanes * n * sizeof(float);
+        const size_t bytes = (size_t)grad_blocks(rows, w) * 2 * w.vecs * w.lanes * n * sizeof(float);
         most = bytes > most ? bytes : most;
     }
     return most;
@@ -551,8 +587,8 @@ hipError_t launch_norm(const NormArgs<T>& a, hipStream_t s) {
 
 size_t layernorm_grad_workspace(int64_t rows, int64_t cols) { return workspace(rows, cols); }
 
-hipError_t launch_layernorm(const NormArgs<uint16_t>& a, int, hipStream_t s) { return launch_norm(a, s); }
-hipError_t launch_layernorm(const NormArgs<float>& a, int, hipStream_t s) { return launch_norm(a, s); }
+hipError_t launch_layernorm(const NormArgs<uint16_t>& a, hipStream_t s) { return launch_norm(a, s); }
+hipError_t launch_layernorm(const NormArgs<float>& a, hipStream_t s) { return launch_norm(a, s); }
 hipError_t launch_layernorm_grad(const NormGradArgs<uint16_t>& a, hipStream_t s) { return launch_grad(a, s); }
 hipError_t launch_layernorm_grad(const NormGradArgs<float>& a, hipStream_t s) { return launch_grad(a, s); }
 

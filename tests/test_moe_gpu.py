@@ -177,6 +177,44 @@ def test_route_grad_against_differences():
         assert abs((ends[0] - ends[1]) / (2 * step) - (f64(dl) * f64(d)).sum()) < size * (16 * U / step + 16 * step ** 2)
 
 
+def test_route_past_32_bits():
+    ld, T, E, k = 1 << 22, 300, 40, 3                        # 5 GB
+    buf = torch.empty(T, ld, device="cuda")
+    l = logits(T, E, F32, 1)
+    v = buf[:, 64:64 + E]
+    v.copy_(l)
+    out = {n: torch.empty(T, k, dtype=d, device="cuda") for n, d in (("gates", F32), ("choice", INT), ("slots", INT))}
+    out |= {n: torch.empty(E + 1, dtype=INT, device="cuda") for n in ("offsets", "counts")}
+    out["loss"] = torch.empty(1, device="cuda")
+    ws = torch.empty(dg.gemm_moe_route_workspace_size(T, E, k), dtype=torch.uint8, device="cuda")
+    dg.moe_route(v, out["gates"], out["choice"], out["slots"], out["offsets"], out["counts"], ws, out["loss"])
+    check_route(out, l, k, True)
+    dl, d = buf[:, 256:256 + E], torch.randn(T, k, generator=gen(2))
+    dg.moe_route_grad(v, out["choice"], out["counts"], dl, d.cuda())
+    want, mag = route_grad_ref(f64(l), f64(out["choice"]).astype(int), f64(out["counts"]).astype(int), f64(d), None, True)
+    rel = 4 * prob_rel(f64(l)).max(1, keepdims=True) + (chain(E) + k + 16) * U
+    assert worst(dl, want, rel * mag + 2 * U * np.abs(want) + 1e-37) <= 1
+
+
+def test_conveniences_refuse_what_the_calls_cannot_take():
+    x, f = torch.zeros(4, 8, dtype=BF16, device="cuda"), torch.zeros(4, device="cuda")
+    i, g = torch.zeros(4, 2, dtype=INT, device="cuda"), torch.zeros(4, 2, device="cuda")
+    for call in (lambda: dg.layernorm(x, x[:3]), lambda: dg.layernorm(x, x.float()), lambda: dg.layernorm(x, x, weight=f),
+                 lambda: dg.layernorm(x.t(), x.t()), lambda: dg.layernorm_grad(x, x, x, f, f[:3]),
+                 lambda: dg.dropout(x, x, 0.1, f), lambda: dg.moe_gather(x, i.t(), x), lambda: dg.moe_gather(x, i[:3], x),
+                 lambda: dg.moe_combine(x, i, x, gates=g[:, :1]), lambda: dg.moe_combine_grad(x, i, x, dgates=g),
+                 lambda: dg.moe_combine(x[:1].expand(4, 8), i, x[:1].expand(4, 8))):
+        with pytest.raises((TypeError, ValueError)):
+            call()
+    ws = torch.zeros(1024, dtype=torch.uint8, device="cuda")
+    for call in (lambda: dg.layernorm(x, x, eps=-1.0), lambda: dg.dropout(x, x, 1.5, torch.zeros(2, dtype=torch.int64, device="cuda")),
+                 lambda: dg.layernorm_grad(x, x, x, f, f, dweight=torch.zeros(8, device="cuda")),
+                 lambda: dg.layernorm_grad(x, x, x, f, f, dweight=torch.zeros(8, device="cuda"), workspace=ws[1:])):
+        with pytest.raises(dg.GemmError) as bad:
+            call()
+        assert bad.value.status == dg.GEMM_ERR_INVALID_VALUE
+
+
 # ---- rows ------------------------------------------------------------------------
 
 def slots_of(T, k, seed, absent=0.1, spare=5):

@@ -67,6 +67,8 @@ def test_norm(rows, cols, dtype, aligned):
     assert worst(mean[:rows], m, am) <= 1 and worst(rstd[:rows], r, ar) <= 1
     assert mean[rows] == 7 and rstd[rows] == 7
     assert untouched(ybuf, rows, cols, ld + 1 - aligned, off)
+    dg.layernorm(xv, xv, w.cuda(), b.cuda(), 1e-5)                     # in place: the same bits
+    assert torch.equal(xv, yv)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -156,7 +158,7 @@ def run_grad(rows, cols, dtype, aligned, res, beta, use_w=True, wants=(True, Tru
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_norm_grad_forms(dtype):
-    for rows, cols in ((37, 200), (9, 3000), (600, 520), (11, 20000)):
+    for rows, cols in ((37, 200), (9, 3000), (600, 520), (11, 20000), (70, 100), (2100, 1031), (300, 5001), (5, 40000)):
         note(f"norm gradient forms {rows} x {cols} {dtype}")
         run_grad(rows, cols, dtype, True, True, 0.0, use_w=False)
         run_grad(rows, cols, dtype, True, False, 1.0, wants=(True, False))
