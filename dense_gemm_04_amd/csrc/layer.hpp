@@ -99,6 +99,7 @@ struct RowsArgs {
     const uint16_t* Y; int64_t ldy;          // combine, gradient
     uint16_t* out; int64_t ldo;              // gather: Y; combine: C; gradient: dY
     float* dgates;                           // gradient, or null
+    bool once;                               // Y's rows are whole cache lines, read past the caches
 };
 hipError_t launch_gather(const RowsArgs& a, hipStream_t s);
 hipError_t launch_combine(const RowsArgs& a, hipStream_t s);
@@ -126,6 +127,10 @@ struct Vec<uint16_t> {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             w[q] = (2 * q < valid ? (uint32_t)p[2 * q] : 0u) | ((2 * q + 1 < valid ? (uint32_t)p[2 * q + 1] : 0u) << 16);
+    }
+    // A whole vector that is not kept in the caches.
+    __device__ __forceinline__ void load_once(const uint16_t* p) {
+        w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p));
     }
     __device__ __forceinline__ void set(const float* v) {
 #pragma unroll

@@ -18,6 +18,22 @@ namespace {
 constexpr int kVec = Vec<uint16_t>::n;
 constexpr int kColumns = 256 * kVec;             // of a workgroup at a time
 
+// A vector of a sorted row. Its last reader in a pass is combine, and in the
+// backward pass combine's gradient, so rows of whole cache lines are read past
+// the caches and leave what is there to the next products. One MI355X, 16 experts, cached
+// and past the caches: product, combine and norm of 2048 tokens x 2048, 8 choices 182 and
+// 174 us, of 8192 x 4096, 2 choices 620 and 616; the gradient, its product and the sum after
+// it 195 and 175, 638 and 618; alone, combine of 4096 x 2048, 8 choices 34.5 and
+// 29.4. Rows that share lines lose by it (a pass over rows of 4092 bytes 13.4 and 17.6).
+// Stores past the caches are not used: alone they gain more (gather of 8191 x 4096,
+// 2 choices 41 and 31), but the product that reads the rows next loses it (with it 556
+// and 566).
+__device__ __forceinline__ void load_sorted(Vec<uint16_t>& v, const RowsArgs& a, int slot, int64_t c, int valid) {
+    const uint16_t* p = a.Y + slot * a.ldy + c;
+    if (a.once) v.load_once(p);
+    else v.load(p, valid);
+}
+
 // A token's slots as scalars: -1 where absent, outside the rows or past k.
 template <int K>
 __device__ __forceinline__ void load_slots(const RowsArgs& a, int64_t t, int* slot) {
@@ -61,7 +77,7 @@ __device__ __forceinline__ void combine_one(const RowsArgs& a, int64_t t, int64_
 #pragma unroll
     for (int j = 0; j < K; ++j) {
         y[j].w = u32x4{0, 0, 0, 0};
-        if (slot[j] >= 0) y[j].load(a.Y + slot[j] * a.ldy + c, valid);
+        if (slot[j] >= 0) load_sorted(y[j], a, slot[j], c, valid);
     }
     if (a.X != nullptr) r.load(a.X + t * a.ldx + c, valid);
 #pragma unroll
@@ -105,7 +121,7 @@ __device__ __forceinline__ void combine_grad_one(const RowsArgs& a, int64_t t, f
 #pragma unroll
             for (int j = 0; j < K; ++j) {
                 y[j].w = u32x4{0, 0, 0, 0};
-                if (slot[j] >= 0) y[j].load(a.Y + slot[j] * a.ldy + c, valid);
+                if (slot[j] >= 0) load_sorted(y[j], a, slot[j], c, valid);
             }
         }
 #pragma unroll
@@ -150,6 +166,11 @@ hipError_t with_choices(int k, F&& launch) {
     return launch(std::integral_constant<int, 16>{});
 }
 
+bool whole_lines(const RowsArgs& a) {
+    constexpr int64_t kLine = 128;
+    return reinterpret_cast<uintptr_t>(a.Y) % kLine == 0 && 2 * a.ldy % kLine == 0 && 2 * a.cols % kLine == 0;
+}
+
 dim3 rows_grid(const RowsArgs& a) {
     const int64_t chunks = (a.cols + kColumns - 1) / kColumns;
     return dim3((unsigned)(chunks < 64 ? chunks : 64), (unsigned)(a.tokens < 65535 ? a.tokens : 65535));
@@ -160,10 +181,14 @@ dim3 rows_grid(const RowsArgs& a) {
 hipError_t launch_gather(const RowsArgs& a, hipStream_t s) {
     return with_choices(a.k, [&](auto k) { return launch_kernel(&rows<k(), false>, rows_grid(a), dim3(256), s, a); });
 }
-hipError_t launch_combine(const RowsArgs& a, hipStream_t s) {
+hipError_t launch_combine(const RowsArgs& args, hipStream_t s) {
+    RowsArgs a = args;
+    a.once = whole_lines(a);
     return with_choices(a.k, [&](auto k) { return launch_kernel(&rows<k(), true>, rows_grid(a), dim3(256), s, a); });
 }
-hipError_t launch_combine_grad(const RowsArgs& a, hipStream_t s) {
+hipError_t launch_combine_grad(const RowsArgs& args, hipStream_t s) {
+    RowsArgs a = args;
+    a.once = whole_lines(a);
     return with_choices(a.k, [&](auto k) {
         return launch_kernel(&combine_grad<k()>, dim3(grid_for(a.tokens)), dim3(256), s, a);
     });
