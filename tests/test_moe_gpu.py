@@ -230,17 +230,18 @@ ROWS = [(1, 1, 1), (1, 8, 4096), (3, 2, 7), (16, 4, 64), (5, 3, 9), (64, 2, 200)
         (130, 1, 2050), (9, 5, 4099), (300, 2, 4096), (6, 7, 8192), (4, 2, 20001), (1100, 4, 256)]
 
 
-@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("layout", ["lines", "aligned", "odd"])
 @pytest.mark.parametrize("T,k,cols", ROWS)
-def test_rows(T, k, cols, aligned):
-    note(f"rows {T} k {k} cols {cols} aligned {aligned}")
+def test_rows(T, k, cols, layout):
+    note(f"rows {T} k {k} cols {cols} {layout}")
     g = gen(T + cols)
     slots, rows = slots_of(T, k, T)
     slots[0, 0] = rows if T > 1 else slots[0, 0]                   # past the rows: absent
     sc = slots.cuda()
     s = slots.long().numpy()
     there = (s >= 0) & (s < rows)
-    ld, off = (-(-cols // 8) * 8 + 8, 0) if aligned else (cols + 1, 1)
+    # Whole cache lines (where the columns are), 16 bytes, and neither.
+    ld, off = {"lines": (-(-cols // 64) * 64 + 64, 0), "aligned": (-(-cols // 8) * 8 + 8, 0), "odd": (cols + 1, 1)}[layout]
     bf = lambda *shape: torch.randn(*shape, generator=g).to(BF16)
     x, y, r, gates = bf(T, cols), bf(rows, cols), bf(T, cols), torch.rand(T, k, generator=g)
     named = np.zeros(rows, dtype=bool)
