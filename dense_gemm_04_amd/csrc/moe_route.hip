@@ -23,6 +23,10 @@
 // for itself: the table is small) and the offsets. Up to kAlone tokens one
 // workgroup does it all in one launch. No sum depends on the order of
 // execution.
+//
+// Neither memory nor the vector unit bounds it, but the way through both: 16384
+// tokens x 128 experts, 8 choices 8.5 us (4 of them vector instructions) and 7.6
+// for 10 MB, 16 x 32, 2 choices 4.7, the gradient of 8191 x 64 3.9.
 
 #include "layer.hpp"
 
@@ -476,8 +480,8 @@ __global__ __launch_bounds__(N) void place(RouteArgs<T> a, Table table, int rows
     finish<N>(a, total, first, sums, red);
 }
 
-// The gradient, L lanes to a token. The choices' gradients reach the lanes that
-// hold their experts through LDS.
+// The gradient, L lanes to a token, whose softmax is taken again from its logits. The
+// choices' gradients reach the lanes that hold their experts through LDS.
 template <typename T, int L, int V>
 __global__ __launch_bounds__(256) void route_grad(RouteGradArgs<T> a) {
     struct Chosen {

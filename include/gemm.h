@@ -487,7 +487,7 @@ gemm_status_t gemm_bf16_grouped_wgrad_f32(int64_t groups, int64_t M, int64_t N, 
  * order and back, with their gradients. Matrices are row-major with a leading
  * dimension as everywhere here; every alignment is taken, and rows on 16 bytes
  * are the fastest. Everything between the operands and a result is formed in
- * fp32 and rounded once. No call uses atomics: the same call gives the same bits.
+ * fp32 and rounded once. The same call gives the same bits.
  * Streams, errors and ownership are those of the other calls. An output may be
  * the same matrix (base and leading dimension) as an input only where said;
  * other overlaps give undefined results.
@@ -618,7 +618,7 @@ gemm_status_t gemm_moe_route_grad_f32(int64_t tokens, int64_t experts, int k, in
  * sorted matrix Y (or dY) is allocated with; ones that no slot names are neither
  * read nor written. k: 1 .. GEMM_MOE_MAX_K.
  *
- *   gather:        Y(slot_tj,:) <- X(t,:)                  two equal slots leave either's row
+ *   gather:        Y(slot_tj,:) <- X(t,:)        (of two equal slots each column keeps either's value)
  *   combine:       C(t,:) <- R(t,:) + sum_j gates[t,j] * Y(slot_tj,:)
  *   its gradient:  dY(slot_tj,:) <- gates[t,j] * dC(t,:),
  *                  dgates[t,j] <- sum over columns of dC(t,:) * Y(slot_tj,:)
