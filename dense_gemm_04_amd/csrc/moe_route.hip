@@ -257,14 +257,15 @@ __device__ __forceinline__ void merge_row(double* v) {
     }
 }
 
-// What choose leaves for place, for each workgroup: its counts (and its tokens
-// with a choice at [experts]) and its sums of p.
+// What choose leaves for place, for each workgroup: its counts, its sums of p and
+// its tokens with a choice.
 struct Table {
     uint16_t* counts;       // workgroups x stride
     float* sums;            // workgroups x stride
-    int stride;
+    int32_t* some;          // workgroups
+    int stride;             // experts rounded up to 4
 };
-inline __host__ __device__ int table_stride(int experts) { return (experts + 1 + 3) & ~3; }
+inline int table_stride(int experts) { return (experts + 3) & ~3; }
 
 // Exclusive sums of counts[0 .. experts - 1] into first[0 .. experts], by one wave.
 __device__ __forceinline__ void scan_counts(const int* counts, int* first, int experts, int lane) {
@@ -283,12 +284,12 @@ __device__ __forceinline__ void scan_counts(const int* counts, int* first, int e
 // Offsets, counts and loss from the counts and sums of p over all tokens, by one
 // workgroup; `red` has a float for each of its waves.
 template <int THREADS, typename T>
-__device__ __forceinline__ void finish(const RouteArgs<T>& a, const int* counts, const int* first, const float* sums,
-                                       float* red) {
+__device__ __forceinline__ void finish(const RouteArgs<T>& a, const int* counts, const int* first, int tokens,
+                                       const float* sums, float* red) {
     const int t = threadIdx.x;
     for (int e = t; e <= a.experts; e += THREADS) {
         a.offsets[e] = first[e];
-        a.counts[e] = counts[e];
+        a.counts[e] = e < a.experts ? counts[e] : tokens;
     }
     if (a.loss == nullptr) return;
     float s = 0.f;
@@ -299,7 +300,7 @@ __device__ __forceinline__ void finish(const RouteArgs<T>& a, const int* counts,
     if (t != 0) return;
     s = 0.f;
     for (int w = 0; w < THREADS / 64; ++w) s += red[w];
-    const int all = first[a.experts], tokens = counts[a.experts];
+    const int all = first[a.experts];
     *a.loss = (float)a.experts * (s / (float)(all > 1 ? all : 1)) / (float)(tokens > 1 ? tokens : 1);
 }
 
@@ -320,7 +321,7 @@ __global__ __launch_bounds__(kThreads) void choose(RouteArgs<T> a, Table table, 
     const int64_t hi = lo + rows < a.tokens ? lo + rows : a.tokens;
     float psum[V] = {};
     for (int e = t; e <= a.experts; e += kThreads) total[e] = 0;
-    int some = 0;                                   // tokens with a choice, in a row's first lane
+    int some = 0;                                   // the wave's tokens with a choice
     for (int64_t base = lo; base < hi; base += kChunk) {
         for (int e = t; e < a.experts; e += kThreads) bits[e] = 0;
         __syncthreads();
@@ -355,7 +356,7 @@ __global__ __launch_bounds__(kThreads) void choose(RouteArgs<T> a, Table table, 
                     a.gates[token * a.k + lane] = bad ? inv : (go ? (a.renormalize ? p / sum : p * inv) : 0.f);
                 }
             }
-            some += go && lane == 0;
+            some += __builtin_popcountll(__ballot(go && lane == 0));
         }
         __syncthreads();
         const int have = (int)(hi - base < kChunk ? hi - base : kChunk) * a.k;
@@ -367,7 +368,7 @@ __global__ __launch_bounds__(kThreads) void choose(RouteArgs<T> a, Table table, 
         for (int e = t; e < a.experts; e += kThreads) total[e] += __builtin_popcountll(bits[e]);
     }
     __syncthreads();
-    if (lane == 0 && some != 0) atomicAdd(&total[a.experts], some);
+    if (lane64 == 0) atomicAdd(&total[a.experts], some);
     if (a.loss != nullptr) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -386,7 +387,8 @@ __global__ __launch_bounds__(kThreads) void choose(RouteArgs<T> a, Table table, 
         }
     if (!alone) {
         for (int e = t; e < table.stride; e += kThreads)
-            table.counts[(int64_t)blockIdx.x * table.stride + e] = e <= a.experts ? (uint16_t)total[e] : 0;
+            table.counts[(int64_t)blockIdx.x * table.stride + e] = e < a.experts ? (uint16_t)total[e] : 0;
+        if (t == 0) table.some[blockIdx.x] = total[a.experts];
         return;
     }
     if (t < 64) scan_counts(total, first, a.experts, t);
@@ -395,18 +397,20 @@ __global__ __launch_bounds__(kThreads) void choose(RouteArgs<T> a, Table table, 
         const int e = a.choice[i];
         if (e >= 0) a.slots[i] += first[e];
     }
-    finish<kThreads>(a, total, first, sums[0], red);
+    finish<kThreads>(a, total, first, total[a.experts], sums[0], red);
 }
 
 // Slots, from each workgroup's counts: those of the workgroups before this one
 // and all of them. One workgroup more, the last, writes offsets, counts and loss.
 // The tables are read by up to kSets sets of threads, 4 columns to a thread; a
 // column's sets are added by one thread. N threads: 512, or 1024 above 128 experts
-// (16384 tokens x 128 experts 7.7 us with 512, 8.1 with 1024; x 256 12.7 and 11.0).
+// (16384 tokens x 128 experts 7.0 us with 512, 7.5 with 1024; x 256 12.7 and 10.3).
+// LDS additions to one address cost 8 ns each, so what many threads add up goes
+// through lanes or sets first.
 constexpr int kSets = 32;
 template <typename T, int N>
 __global__ __launch_bounds__(N) void place(RouteArgs<T> a, Table table, int rows, int blocks) {
-    __shared__ int before[kMaxExperts + 4], total[kMaxExperts + 4], first[kMaxExperts + 1];
+    __shared__ int before[kMaxExperts], total[kMaxExperts], first[kMaxExperts + 1], tokens;
     __shared__ float sums[kMaxExperts], red[N / 64];
     __shared__ u32x4 part[2][N];
     const int t = threadIdx.x, words = table.stride / 4, sets = N / words < kSets ? N / words : kSets;
@@ -418,6 +422,11 @@ __global__ __launch_bounds__(N) void place(RouteArgs<T> a, Table table, int rows
     if (lo + t < hi) {
         e0 = a.choice[lo + t];
         s0 = a.slots[lo + t];
+    }
+    int some = 0;                       // by the last wave, which has the fewest columns
+    if (last && t >= N - 64) {
+#pragma unroll 4
+        for (int b = t - (N - 64); b < blocks; b += 64) some += table.some[b];
     }
     // Two 16-bit counts to an addition, for as many rows as cannot overflow them: the
     // vector unit, not memory, is what every workgroup's sum of the whole table
@@ -448,6 +457,11 @@ __global__ __launch_bounds__(N) void place(RouteArgs<T> a, Table table, int rows
             psum += *reinterpret_cast<const f32x4*>(table.sums + (int64_t)b * table.stride + 4 * (t % words));
     }
     __syncthreads();
+    if (last && t >= N - 64) {
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) some += __shfl_xor(some, d, 64);
+        tokens = some;
+    }
     for (int e = t; e < table.stride; e += N) {
         const uint32_t* p = reinterpret_cast<const uint32_t*>(part) + e;
         int all = 0, mine = 0;
@@ -477,7 +491,7 @@ __global__ __launch_bounds__(N) void place(RouteArgs<T> a, Table table, int rows
         sums[e] = v;
     }
     __syncthreads();
-    finish<N>(a, total, first, sums, red);
+    finish<N>(a, total, first, tokens, sums, red);
 }
 
 // The gradient, L lanes to a token, whose softmax is taken again from its logits. The
@@ -572,7 +586,20 @@ int rows_each(int tokens) {
     return (int)(rows < kMostRows ? rows : kMostRows);
 }
 int64_t blocks_of(int tokens) { return ((int64_t)tokens + rows_each(tokens) - 1) / rows_each(tokens); }
-size_t sums_at(int64_t blocks, int experts) { return ((size_t)blocks * table_stride(experts) * 2 + 255) & ~(size_t)255; }
+
+// The tables one after another, each from a multiple of 256 bytes on.
+struct Layout {
+    size_t sums, some, bytes;
+};
+Layout layout_of(int64_t blocks, int experts) {
+    const auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    const size_t each = (size_t)blocks * table_stride(experts);
+    Layout l;
+    l.sums = up(each * 2);
+    l.some = l.sums + up(each * 4);
+    l.bytes = l.some + up((size_t)blocks * 4) + 256;
+    return l;
+}
 
 template <typename T, int L, int V, int K>
 hipError_t launch_choose(const RouteArgs<T>& a, const Table& table, hipStream_t s) {
@@ -600,7 +627,9 @@ hipError_t launch(const RouteArgs<T>& a, hipStream_t s) {
     Table table;
     table.stride = table_stride(a.experts);
     table.counts = static_cast<uint16_t*>(a.ws);
-    table.sums = reinterpret_cast<float*>(static_cast<char*>(a.ws) + sums_at(blocks_of(a.tokens), a.experts));
+    const Layout l = layout_of(blocks_of(a.tokens), a.experts);
+    table.sums = reinterpret_cast<float*>(static_cast<char*>(a.ws) + l.sums);
+    table.some = reinterpret_cast<int32_t*>(static_cast<char*>(a.ws) + l.some);
     if (a.experts <= 16) return launch_choose<T, 16, 1>(a, table, s);
     if (a.experts <= 32) return launch_choose<T, 16, 2>(a, table, s);
     if (a.experts <= 64) return launch_choose<T, 16, 4>(a, table, s);
@@ -626,8 +655,7 @@ hipError_t launch_grad(const RouteGradArgs<T>& a, hipStream_t s) {
 }  // namespace
 
 size_t route_workspace(int64_t tokens, int64_t experts, int) {
-    const int64_t blocks = blocks_of((int)tokens);
-    return sums_at(blocks, (int)experts) + (size_t)blocks * table_stride((int)experts) * sizeof(float) + 256;
+    return layout_of(blocks_of((int)tokens), (int)experts).bytes;
 }
 
 hipError_t launch_route(const RouteArgs<uint16_t>& a, hipStream_t s) { return launch(a, s); }
