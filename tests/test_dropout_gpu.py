@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import dense_gemm_04_amd as dg
-from layer_util import BF16, F32, STEP, U, dropout_ref, worst
+from layer_util import BF16, F32, STEP, U, dropout_ref, philox, worst
 from ops_util import f64, gen
 from test_norm_gpu import layout, note, place, rows_of, untouched
 
@@ -42,6 +42,10 @@ def test_dropout(rows, cols, p, dtype, aligned):
         assert untouched(buf, rows, cols, ld, off)
         if res is None:
             assert np.array_equal(f64(yv) != 0, keep & (f64(x) != 0))
+    # In the residual's place, the same bits.
+    again, av = place(r, dtype, ld, off)
+    dg.dropout(xv, av, p, rng(), av)
+    assert torch.equal(av, yv)
     # The mask is the same whatever the type and layout, and in place.
     dg.dropout(xv, xv, p, rng())
     assert np.array_equal(f64(xv) != 0, keep & (f64(x) != 0))
@@ -121,3 +125,16 @@ def test_dropout_past_32_bits():
     dg.dropout(buf[:, :cols], buf[:, 128:128 + cols], 0.1, rng())
     want, _ = dropout_ref(f64(x), None, 0.1, SEED, OFFSET)
     assert worst(buf[:, 128:128 + cols], want, allow(f64(x), None, want, 0.1, BF16)) <= 1
+
+
+def test_dropout_of_more_vectors_than_32_bits_count():
+    """2^32 vectors of 8 columns (69 GB), in place; rows from all over against the generator."""
+    rows, cols = 1 << 20, 1 << 15
+    x = torch.ones(rows, cols, dtype=BF16, device="cuda")
+    dg.dropout(x, x, 0.5, rng(3, 4))
+    torch.cuda.synchronize()
+    ones = np.ones((1, cols // 8), dtype=np.uint64)
+    for row in (0, 1, (1 << 17) - 1, (1 << 19) + 12345, rows - 2, rows - 1):
+        w = philox((np.arange(cols // 8, dtype=np.uint64)[None, :], ones * np.uint64(row), ones * np.uint64(4), 0 * ones), (3, 0))
+        u = np.stack([h for v in w for h in (v & np.uint64(0xFFFF), v >> np.uint64(16))], 2).reshape(cols)
+        assert np.array_equal(f64(x[row]), np.where(u >= 32768, 2.0, 0.0)), row

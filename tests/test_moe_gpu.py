@@ -296,6 +296,24 @@ def test_rows(T, k, cols, layout):
             assert torch.equal(again, dgates) and torch.equal(place_y.cpu()[s[there]], dy.cpu()[s[there]])
 
 
+@pytest.mark.parametrize("T,k,cols", [(70000, 2, 24), (3, 2, 140000), (1100000, 1, 8)])
+def test_rows_past_the_grid(T, k, cols):
+    """More tokens or columns than a launch has workgroups for, each with its own value."""
+    note(f"rows {T} k {k} cols {cols}")
+    slots = torch.randperm(T * k, generator=gen(T)).view(T, k).to(INT).cuda()
+    x = (torch.arange(T, device="cuda")[:, None] % 251 + torch.arange(cols, device="cuda")[None, :] % 5).to(BF16)
+    y = torch.zeros(T * k, cols, dtype=BF16, device="cuda")
+    dg.moe_gather(x, slots, y)
+    assert torch.equal(y[slots.long().flatten()].view(T, k, cols), x[:, None, :].expand(-1, k, -1))
+    c = torch.empty_like(x)
+    dg.moe_combine(y, slots, c, torch.full((T, k), 1.0 / k, device="cuda"))
+    assert torch.equal(c, x)
+    dgates = torch.empty(T, k, device="cuda")
+    dg.moe_combine_grad(x, slots, y, y, None, dgates)
+    want = (x.double() ** 2).sum(1, keepdim=True).expand(-1, k)
+    assert bool(((dgates.double() - want).abs() <= chain(cols) * U * want).all())
+
+
 def test_rows_without_any_row():
     slots = torch.zeros(5, 2, dtype=INT, device="cuda")
     x = torch.randn(5, 40, generator=gen(1)).to(BF16).cuda()

@@ -231,3 +231,26 @@ def test_norm_past_32_bits():
     args = (f64(x), f64(w), f64(mean), f64(rstd), f64(y), None)
     for got, want, allow in zip((dx, dw, db), norm_grad_ref(*args), norm_grad_allow(*args, BF16)):
         assert worst(got, want, allow) <= 1
+
+
+def test_norm_of_more_rows_than_one_launch_takes():
+    """2^27 short rows and a few, in place; the ends and rows between against a call on them alone."""
+    rows, cols = (1 << 27) + 5, 8
+    part = torch.randn(1 << 20, cols, generator=gen(6)).to(BF16).cuda()
+    x = part.repeat(rows // part.shape[0] + 1, 1)[:rows]
+    rstd = torch.zeros(rows, device="cuda")
+    w = torch.randn(cols, generator=gen(7)).to(BF16).cuda()
+    alone, r = torch.empty_like(part), torch.empty(part.shape[0], device="cuda")
+    dg.layernorm(part, alone, w, None, 1e-5, None, r)
+    dg.layernorm(x, x, w, None, 1e-5, None, rstd)
+    torch.cuda.synchronize()
+    args = (f64(part[:1000]), f64(w), None, 1e-5)
+    for lo in (0, 5 << 20, 127 << 20, rows - 1005):
+        at = lo % part.shape[0]
+        some = part[at:at + 1000] if at + 1000 <= part.shape[0] else None
+        if some is None:                                  # across the repeats' border
+            some = torch.cat([part[at:], part[:1000 - (part.shape[0] - at)]])
+        args = (f64(some), f64(w), None, 1e-5)
+        assert worst(x[lo:lo + 1000], norm_ref(*args)[0], norm_allow(*args, BF16)[0]) <= 1
+        assert worst(rstd[lo:lo + 1000], norm_ref(*args)[2], norm_allow(*args, BF16)[2]) <= 1
+    assert bool((rstd > 0).all())
