@@ -741,6 +741,8 @@ bool choices_ok(int64_t tokens, int k, int64_t most) {
     return size_ok(tokens) && k >= 1 && k <= most && tokens * k <= INT_MAX;
 }
 
+static_assert(GEMM_MOE_MAX_EXPERTS == dg::kMaxExperts && GEMM_MOE_MAX_K == dg::kMaxChoices, "the kernels' limits");
+
 bool route_sizes_ok(int64_t tokens, int64_t experts, int k) {
     return experts >= 1 && experts <= GEMM_MOE_MAX_EXPERTS &&
            choices_ok(tokens, k, experts < GEMM_MOE_MAX_K ? experts : GEMM_MOE_MAX_K);

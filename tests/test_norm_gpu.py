@@ -14,7 +14,8 @@ pytestmark = pytest.mark.gpu
 # Rows x cols: every width class of the kernels and its edges, few and many rows.
 SIZES = [(1, 1), (5, 2), (3, 7), (300, 8), (7, 9), (1000, 63), (33, 64), (64, 129), (257, 255), (1030, 256), (3, 511),
          (129, 513), (2, 1000), (4095, 1023), (700, 1024), (1, 2048), (530, 2050), (16, 4096), (1025, 4095), (40, 4104),
-         (9, 8191), (260, 8192), (3, 12288), (17, 16384), (5, 16392), (2, 32768), (300, 20001), (3, 70001)]
+         (9, 8191), (260, 8192), (3, 12288), (17, 16384), (5, 16392), (2, 32768), (300, 20001), (3, 70001),
+         (70, 1500), (33, 3000), (40, 5000), (37, 6100), (19, 10000), (12, 22000), (6, 26000), (9, 30001)]
 
 
 def note(text):
@@ -118,8 +119,9 @@ def test_norm_of_rows_that_are_not_finite(cols):
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("rows,cols", SIZES)
 def test_norm_grad(rows, cols, dtype, aligned):
-    note(f"norm gradient {rows} x {cols} {dtype} aligned {aligned}")
-    run_grad(rows, cols, dtype, aligned, res=bool((rows + cols) % 2), beta=0.5 if cols % 3 else 0.0)
+    for res in (False, True):
+        note(f"norm gradient {rows} x {cols} {dtype} aligned {aligned} residual {res}")
+        run_grad(rows, cols, dtype, aligned, res=res, beta=0.5 if (cols % 3 == 0) == res else 0.0)
 
 
 def run_grad(rows, cols, dtype, aligned, res, beta, use_w=True, wants=(True, True), alias=None):
