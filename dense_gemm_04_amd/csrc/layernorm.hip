@@ -253,6 +253,15 @@ struct RowOf {
         r = a.rstd[row];
         m = a.mean[row];
     }
+    // Waits for every load of the row: a volatile statement that takes their
+    // results and stays ahead of the barrier after it.
+    __device__ __forceinline__ void landed() const {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            asm volatile("" ::"v"(x[i].w), "v"(dy[i].w));
+            if constexpr (RES) asm volatile("" ::"v"(res[i].w));
+        }
+    }
 };
 
 template <typename T, int L, int V, bool RES, bool PRE>
@@ -301,7 +310,9 @@ __global__ __launch_bounds__(512, 2) void norm_grad(NormGradArgs<T> a) {
     // Every lane stores whole vectors: where the last ones of a row overlap, they
     // hold the same bits. With that a turn's loads and stores are the same in
     // number on every path, and the wait for a row's loads leaves the
-    // stores before and the loads after them in flight.
+    // stores before and the loads after them in flight. dX may be dY or R, so
+    // all the row's loads have to land before any wave stores to it: each wave
+    // waits for its own before the barrier, which orders LDS alone.
     const auto one = [&](bool on) {
         float sg = 0.f, sgh = 0.f;
         if (on) {
@@ -328,6 +339,7 @@ __global__ __launch_bounds__(512, 2) void norm_grad(NormGradArgs<T> a) {
             sg = wave_sum(sg);
             sgh = wave_sum(sgh);
             if constexpr (kWaves > 1) {
+                now.landed();
                 if ((t & 63) == 0) {
                     part[turn][wave][0] = sg;
                     part[turn][wave][1] = sgh;
