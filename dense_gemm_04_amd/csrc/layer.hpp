@@ -233,6 +233,16 @@ __device__ __forceinline__ float add_lanes(float v) {
     both_lanes<APART>(__builtin_bit_cast(uint32_t, v), x, y);
     return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
 }
+
+// What a wave's lanes wrote to LDS before is seen by its other lanes behind. They
+// run in step, so this costs no instruction: it keeps the compiler from moving
+// LDS accesses across.
+__device__ __forceinline__ void lds_wave_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // Workgroups for `units` independent pieces: as many, up to what a grid
 // dimension takes; the kernels stride over the rest.
 inline unsigned grid_for(int64_t units) {

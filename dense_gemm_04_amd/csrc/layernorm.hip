@@ -471,7 +471,7 @@ __global__ __launch_bounds__(256) void sum_images(const f32x4* images, int count
 #pragma unroll
     for (int g = 1; g < 8; ++g) s += part[(t >> 2) + 8 * g][t & 3];
     part[t >> 2][t & 3] = s;
-    __builtin_amdgcn_wave_barrier();
+    lds_wave_barrier();
     if (t >= 4) return;
 #pragma unroll
     for (int g = 1; g < 8; ++g) s += part[g][t];

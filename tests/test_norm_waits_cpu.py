@@ -120,3 +120,17 @@ def test_rows_of_several_waves_are_whole_before_their_barrier(tmp_path):
     # 3 to 8 vectors of bf16 (above 4 with 512 lanes alone), 5 to 8 of fp32; with and without R.
     assert checked == 2 * (2 + 2 + 6 + 3 * 4)
     assert not bad, bad
+
+
+def test_lanes_that_exchange_through_lds_order_it():
+    """A barrier of a wave's lanes orders no memory by itself: it stands between a release and an
+    acquire of LDS, also where the lanes run in step."""
+    fence = r'__builtin_amdgcn_fence\(__ATOMIC_{}, "(?:wavefront|workgroup)", "local"\);\s*'
+    whole = re.compile(fence.format("RELEASE") + r"__builtin_amdgcn_wave_barrier\(\);\s*" + fence.format("ACQUIRE"))
+    bare = {}
+    for name in sorted(os.listdir(build.CSRC)):
+        text = open(os.path.join(build.CSRC, name), encoding="utf-8").read()
+        left = whole.sub("", text).count("wave_barrier")
+        if left != text.count("lds_wave_barrier"):
+            bare[name] = left
+    assert not bare, bare
