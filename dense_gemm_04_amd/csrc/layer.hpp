@@ -212,6 +212,16 @@ __device__ __forceinline__ float wave_sum(float v) {
     v = dpp_add<0x143, 0xc>(v);        // rows 2 and 3 take the first half
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
+// Sums of two values over the wave, as scalars: half the lanes go on with each.
+__device__ __forceinline__ void wave_sums(float& a, float& b) {
+    const auto w = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b),
+                                                    false, false);
+    const uint32_t x = w[0], y = w[1];                 // lower half: a's, upper half: b's
+    float v = sum_of_16(__builtin_bit_cast(float, x) + __builtin_bit_cast(float, y));
+    v = dpp_add<0x142, 0xa>(v);
+    a = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 31));
+    b = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
 
 // A value and that of the lane 16 or 32 lanes away: of both results, one is v
 // and the other the partner's, alike in both lanes.

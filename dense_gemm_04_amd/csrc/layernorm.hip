@@ -6,10 +6,13 @@
 //
 // Bound by memory: X is read once and Y written once, X, dY (and R) read and dX
 // written once, with every value in registers between a row's sums and its
-// result. The two passes over the registers (mean first, then the squares of the
-// differences) keep rows far from zero exact. Rows whose columns are not whole
-// vectors read their last n columns again, at whatever alignment, and count each
-// once.
+// result. The second pass over the registers sums the differences from the first
+// one's mean beside their squares: what the mean lost in its sum and in rounding
+// to fp32 goes into y and the variance, so that rows far from zero come out as
+// exact as others (4096 columns around 4096, spread 1: y off by 5.6e-4 without it,
+// 5.6e-7 with it). The gradients take the mean rounded to fp32. Rows whose columns
+// are not whole vectors read their last n columns again, at whatever alignment,
+// and count each once.
 //
 // One MI355X: the norm of 8192 x 4096 bf16 25 us (5.4 TB/s; a copy of as much
 // 26.5), its gradients with a residual 53 us and 5 for the last sums (5.0 TB/s over
@@ -19,6 +22,17 @@
 
 namespace dg {
 namespace {
+
+// What is left of a row's mean after its first estimate m, and 1 / the deviation, from the
+// sums of x - m and of their squares; inv = 1 / columns.
+struct Rest {
+    float mean, rstd;
+    __device__ __forceinline__ Rest(float sum, float squares, float inv, float eps) {
+        mean = sum * inv;
+        const float var = squares * inv - mean * mean;
+        rstd = 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);          // a NaN stays
+    }
+};
 
 // Sum over a workgroup of 256 threads, in every thread. `part`: 4 values of LDS.
 __device__ __forceinline__ float block_sum(float v, float* part) {
@@ -46,7 +60,7 @@ __global__ __launch_bounds__(256) void norm_rows(NormArgs<T> a) {
             for (int e = 0; e < n; ++e) s += v.at(e);
         }
         const float m = block_sum(s, part) / (float)a.cols;
-        s = 0.f;
+        float sd = 0.f, sq = 0.f;
         for (int64_t c = (int64_t)threadIdx.x * n; c < a.cols; c += 256 * n) {
             Vec<T> v;
             const int valid = inside(a.cols, c, n);
@@ -54,12 +68,15 @@ __global__ __launch_bounds__(256) void norm_rows(NormArgs<T> a) {
 #pragma unroll
             for (int e = 0; e < n; ++e) {
                 const float d = v.at(e) - m;
-                s += e < valid ? d * d : 0.f;
+                sd += e < valid ? d : 0.f;
+                sq += e < valid ? d * d : 0.f;
             }
         }
-        const float r = 1.f / sqrtf(block_sum(s, part) / (float)a.cols + a.eps);
+        sd = block_sum(sd, part);
+        const Rest rest(sd, block_sum(sq, part), 1.f / (float)a.cols, a.eps);
+        const float r = rest.rstd, shift = -rest.mean * r;
         if (threadIdx.x == 0) {
-            if (a.mean != nullptr) a.mean[row] = m;
+            if (a.mean != nullptr) a.mean[row] = m + rest.mean;
             if (a.rstd != nullptr) a.rstd[row] = r;
         }
         for (int64_t c = (int64_t)threadIdx.x * n; c < a.cols; c += 256 * n) {
@@ -71,7 +88,7 @@ __global__ __launch_bounds__(256) void norm_rows(NormArgs<T> a) {
             float y[n];
 #pragma unroll
             for (int e = 0; e < n; ++e) {
-                const float h = (v.at(e) - m) * r;
+                const float h = __builtin_fmaf(v.at(e) - m, r, shift);
                 y[e] = __builtin_fmaf(h, a.weight != nullptr ? w.at(e) : 1.f, a.bias != nullptr ? b.at(e) : 0.f);
             }
             v.set(y);
@@ -82,11 +99,12 @@ __global__ __launch_bounds__(256) void norm_rows(NormArgs<T> a) {
 
 // L threads to a row (16, or whole waves), V vectors to a thread: one read of X, whose
 // values stay in registers between the mean, the squares and Y. A wave to a row
-// needs no barrier.
+// needs no barrier. inv: 1 / columns.
 template <typename T, int L, int V>
-__global__ __launch_bounds__(L < 256 ? 256 : L) void norm(NormArgs<T> a) {
+__global__ __launch_bounds__(L < 256 ? 256 : L) void norm(NormArgs<T> a, float inv) {
     constexpr int n = Vec<T>::n, kThreads = L < 256 ? 256 : L, kGroups = kThreads / L, kWaves = L / 64;
-    __shared__ float part[2][kThreads / 64];
+    __shared__ float part[kThreads / 64];
+    __shared__ float2 parts[kThreads / 64];
     const int t = threadIdx.x, lane = t % L, cols = (int)a.cols;
     const int64_t row0 = (int64_t)blockIdx.x * kGroups + t / L;
     const bool on = row0 < a.rows;                      // the others go along to the end
@@ -107,36 +125,53 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm(NormArgs<T> a) {
 #pragma unroll
         for (int i = 0; i < V; ++i) b[i].load(a.bias + col[i], n);
     }
-    const auto row_sum = [&](float v, int turn) {
-        if constexpr (L == 16) return sum_of_16(v);
-        v = wave_sum(v);
-        if constexpr (kWaves > 1) {
-            if ((t & 63) == 0) part[turn][t >> 6] = v;
-            lds_only_barrier();                      // weight and bias stay on their way
-            v = 0.f;
-#pragma unroll
-            for (int q = 0; q < kWaves; ++q) v += part[turn][t / L * kWaves + q];
-        }
-        return v;
-    };
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int e = 0; e < n; ++e) s += i == V - 1 && e < last.skip ? 0.f : x[i].at(e);
-    const float m = row_sum(s, 0) / (float)cols;
-    s = 0.f;
+    s = L == 16 ? sum_of_16(s) : wave_sum(s);
+    if constexpr (kWaves > 1) {
+        if ((t & 63) == 0) part[t >> 6] = s;
+        lds_only_barrier();                      // weight and bias stay on their way
+        s = 0.f;
+#pragma unroll
+        for (int q = 0; q < kWaves; ++q) s += part[t / L * kWaves + q];
+    }
+    // s / columns, as rounded: the rest of the first quotient is exact.
+    float m = s * inv;
+    m = __builtin_fmaf(__builtin_fmaf(-m, (float)cols, s), inv, m);
+    float sd = 0.f, sq = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int e = 0; e < n; ++e) {
             const float d = x[i].at(e) - m;
-            s = i == V - 1 && e < last.skip ? s : __builtin_fmaf(d, d, s);
+            const bool skip = i == V - 1 && e < last.skip;
+            sd += skip ? 0.f : d;
+            sq = skip ? sq : __builtin_fmaf(d, d, sq);
         }
-    const float r = 1.f / sqrtf(row_sum(s, 1) / (float)cols + a.eps);
+    if constexpr (L == 16) {
+        sd = sum_of_16(sd);
+        sq = sum_of_16(sq);
+    } else {
+        wave_sums(sd, sq);
+    }
+    if constexpr (kWaves > 1) {
+        if ((t & 63) == 0) parts[t >> 6] = float2{sd, sq};
+        lds_only_barrier();
+        sd = sq = 0.f;
+#pragma unroll
+        for (int q = 0; q < kWaves; ++q) {
+            sd += parts[t / L * kWaves + q].x;
+            sq += parts[t / L * kWaves + q].y;
+        }
+    }
+    const Rest rest(sd, sq, inv, a.eps);
+    const float r = rest.rstd, shift = -rest.mean * r;
     if (!on) return;
     if (lane == 0) {
-        if (a.mean != nullptr) a.mean[row] = m;
+        if (a.mean != nullptr) a.mean[row] = m + rest.mean;
         if (a.rstd != nullptr) a.rstd[row] = r;
     }
 #pragma unroll
@@ -144,7 +179,7 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm(NormArgs<T> a) {
         float y[n];
 #pragma unroll
         for (int e = 0; e < n; ++e) {
-            y[e] = (x[i].at(e) - m) * r;
+            y[e] = __builtin_fmaf(x[i].at(e) - m, r, shift);
             if (a.weight != nullptr) y[e] *= w[i].at(e);
             if (a.bias != nullptr) y[e] += b[i].at(e);
         }
@@ -581,7 +616,7 @@ hipError_t launch_rows(const NormArgs<T>& a, hipStream_t s) {
     constexpr int kThreads = L < 256 ? 256 : L, kGroups = kThreads / L;
     const int64_t blocks = (a.rows + kGroups - 1) / kGroups;
     if (blocks * kThreads > INT32_MAX) return launch_general(a, s);       // past what a launch takes
-    return launch_kernel(&norm<T, L, V>, dim3((unsigned)blocks), dim3(kThreads), s, a);
+    return launch_kernel(&norm<T, L, V>, dim3((unsigned)blocks), dim3(kThreads), s, a, 1.f / (float)a.cols);
 }
 template <typename T, int L>
 hipError_t launch_rows(const NormArgs<T>& a, int vecs, hipStream_t s) {

@@ -1,0 +1,72 @@
+"""Rows far from zero: what a mean loses in its fp32 sum and rounding reaches neither
+the norm nor its deviation.
+
+Allowances (layer_util's U and chain). A first mean m0 is off by at most
+e = (chain + 2) U mean|x|. Each x - m0 is off by U of itself, so the mean of the differences by
+(chain + 4) U (mean|x - m| + e) (dm); their mean square by (chain + 4) U (var + e^2), of
+which the square of their mean takes off e^2 with 4 U more: (chain + 8) U (var + e^2) (dv).
+rstd is off by half of dv rstd^2, relative, and 4 steps; y by dm rstd, by 4 U for the steps of
+(x - m0) rstd and of the shift, whose magnitudes add up to h + 2 e rstd, and by half a step of its type.
+"""
+import numpy as np
+import pytest
+import torch
+
+import dense_gemm_04_amd as dg
+from layer_util import BF16, F32, STEP, U, chain, norm_ref, worst
+from ops_util import f64, gen
+
+pytestmark = pytest.mark.gpu
+
+# Widths of every kernel: 16 lanes, a wave, 4 and 16 waves to a row (few and many rows), and the general one.
+COLS = [3, 60, 100, 700, 1024, 4096, 5000, 9000, 20000, 40000, 70001]
+
+
+def check(x, dtype, eps):
+    rows, cols = x.shape
+    y = torch.empty(rows, cols, dtype=dtype, device="cuda")
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    dg.layernorm(x.cuda(), y, None, None, eps, mean, rstd)
+    x = f64(x)
+    want, m, r = norm_ref(x, None, None, eps)
+    d = np.abs(x - m[:, None])
+    e = (chain(cols) + 2) * U * np.abs(x).mean(1)
+    dm = (chain(cols) + 4) * U * (d.mean(1) + e)
+    rel = (chain(cols) + 8) * U * ((d * d).mean(1) + e * e) * r * r / 2 + 4 * U
+    h = d * r[:, None]
+    ay = (dm * r)[:, None] + h * rel[:, None] + 4 * U * (h + 2 * (e * r)[:, None]) + (STEP[dtype] + U) * np.abs(want)
+    assert worst(y, want, ay) <= 1
+    assert worst(rstd, r, r * rel) <= 1
+    assert worst(mean, m, dm + 2 * U * np.abs(m)) <= 1
+
+
+@pytest.mark.parametrize("cols", COLS)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_far_from_zero(cols, dtype):
+    g = gen(cols)
+    for far, wide in ((4096.0, 1.0), (-1e5, 3.0)):
+        for rows in (6, 600 if cols <= 9000 else 7):
+            print(f"norm of {rows} x {cols} {dtype} around {far}", flush=True)
+            check((torch.randn(rows, cols, generator=g) * wide + far).to(dtype), dtype, 1e-6)
+
+
+@pytest.mark.parametrize("cols", COLS)
+def test_constant_rows_far_from_zero(cols):
+    """Their norm is 0, up to what the sums of equal differences leave of one."""
+    value = torch.tensor([4096.3, -10000.7, 1e6 / 3, 0.1, 77777.7])
+    check(value[:, None].expand(5, cols).contiguous(), F32, 1e-5)
+
+
+@pytest.mark.parametrize("cols", [3, 60, 700, 4096, 70001])
+def test_rows_past_the_range_of_their_sums(cols):
+    """Finite values whose sums are not: NaN, or a deviation that counts as infinite."""
+    x = torch.randn(4, cols, generator=gen(1)).abs() + 1
+    x[0] *= 1e30
+    x[1] = x[1] * 1e30 + 1e33
+    x[2] = 3e38
+    b = torch.randn(cols, generator=gen(2)).cuda()
+    y, rstd = torch.empty(4, cols, device="cuda"), torch.empty(4, device="cuda")
+    dg.layernorm(x.cuda(), y, None, b, 1e-5, None, rstd)
+    for i in range(3):
+        assert bool(y[i].isnan().all()) or torch.equal(y[i], b) and float(rstd[i]) == 0
+    assert bool(y[3].isfinite().all())
