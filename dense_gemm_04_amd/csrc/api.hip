@@ -733,7 +733,9 @@ gemm_status_t dropout(int64_t rows, int64_t cols, float p, const uint64_t* rng, 
         return GEMM_ERR_INVALID_VALUE;
     if (rows == 0 || cols == 0) return GEMM_OK;
     if (X == nullptr || Y == nullptr || rng == nullptr) return GEMM_ERR_INVALID_VALUE;
-    const dg::DropoutArgs<T> a{rows, cols, (uint32_t)(p * 65536.f + 0.5f), rng, X, ldx, R, ldr, Y, ldy};
+    // In 64 bits: the fp32 value right below 2^-17 would round up to 1 with the half added.
+    const uint32_t drop = (uint32_t)((double)p * 65536. + 0.5);
+    const dg::DropoutArgs<T> a{rows, cols, drop, rng, X, ldx, R, ldr, Y, ldy};
     return on_device([&](int) { return dg::launch_dropout(a, reinterpret_cast<hipStream_t>(stream)); });
 }
 
