@@ -117,14 +117,21 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm(NormArgs<T> a, float i
     Vec<T> x[V], w[V], b[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) x[i].load(a.X + row * a.ldx + col[i], n);
-    if (a.weight != nullptr) {
+    // Weight and bias are on their way beside X where the 128 registers of 1024
+    // threads hold all three; where they would spill, they come after the sums
+    // (1024 x 65536 bf16 98 us, 124 with spilled registers; 512 x 49160 30 and 40).
+    constexpr bool kLate = kThreads == 1024 && sizeof(T) == 2 && V > 6;
+    const auto load_columns = [&] {
+        if (a.weight != nullptr) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) w[i].load(a.weight + col[i], n);
-    }
-    if (a.bias != nullptr) {
+            for (int i = 0; i < V; ++i) w[i].load(a.weight + col[i], n);
+        }
+        if (a.bias != nullptr) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) b[i].load(a.bias + col[i], n);
-    }
+            for (int i = 0; i < V; ++i) b[i].load(a.bias + col[i], n);
+        }
+    };
+    if constexpr (!kLate) load_columns();
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -174,6 +181,7 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm(NormArgs<T> a, float i
         if (a.mean != nullptr) a.mean[row] = m + rest.mean;
         if (a.rstd != nullptr) a.rstd[row] = r;
     }
+    if constexpr (kLate) load_columns();
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         float y[n];

@@ -13,13 +13,13 @@ import pytest
 import torch
 
 import dense_gemm_04_amd as dg
-from layer_util import BF16, F32, STEP, U, chain, norm_ref, worst
+from layer_util import BF16, F32, STEP, U, chain, norm_allow, norm_ref, worst
 from ops_util import f64, gen
 
 pytestmark = pytest.mark.gpu
 
 # Widths of every kernel: 16 lanes, a wave, 4 and 16 waves to a row (few and many rows), and the general one.
-COLS = [3, 60, 100, 700, 1024, 4096, 5000, 9000, 20000, 40000, 70001]
+COLS = [3, 60, 100, 700, 1024, 4096, 5000, 9000, 20000, 40000, 50001, 65536, 70001]
 
 
 def check(x, dtype, eps):
@@ -70,3 +70,17 @@ def test_rows_past_the_range_of_their_sums(cols):
     for i in range(3):
         assert bool(y[i].isnan().all()) or torch.equal(y[i], b) and float(rstd[i]) == 0
     assert bool(y[3].isfinite().all())
+
+
+@pytest.mark.parametrize("cols", [49152, 49153, 57344, 60007, 65536])
+def test_rows_whose_weight_comes_late(cols):
+    """The widest rows of one workgroup, whose weight and bias are read after the sums; in place the same bits."""
+    g = gen(cols)
+    x, w, b = ((torch.randn(*s, generator=g) * 2 + 1).to(BF16).cuda() for s in ((5, cols), (cols,), (cols,)))
+    y = torch.empty_like(x)
+    for ww, bb in ((w, b), (None, b), (w, None), (None, None)):
+        dg.layernorm(x, y, ww, bb)
+        args = f64(x), None if ww is None else f64(w), None if bb is None else f64(b), 1e-5
+        assert worst(y, norm_ref(*args)[0], norm_allow(*args, BF16)[0]) <= 1
+    dg.layernorm(x, x)
+    assert torch.equal(x, y)
