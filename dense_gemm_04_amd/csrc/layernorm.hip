@@ -23,15 +23,25 @@
 namespace dg {
 namespace {
 
+// s / cols as rounded, from inv = 1 / cols: the rest of the first quotient is exact.
+__device__ __forceinline__ float over_cols(float s, float cols, float inv) {
+    const float q = s * inv;
+    return __builtin_fmaf(__builtin_fmaf(-q, cols, s), inv, q);
+}
+
 // What is left of a row's mean after its first estimate m, and 1 / the deviation, from the
-// sums of x - m and of their squares; inv = 1 / columns.
+// means of x - m and of their squares.
 struct Rest {
-    float mean, rstd;
-    __device__ __forceinline__ Rest(float sum, float squares, float inv, float eps) {
-        mean = sum * inv;
-        const float var = squares * inv - mean * mean;
+    float mean, rstd, least;
+    __device__ __forceinline__ Rest(float rest, float squares, float eps) : mean(rest) {
+        const float var = squares - mean * mean;
         rstd = 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);          // a NaN stays
+        least = var * 0x1p-40f;
     }
+    // Up to 2^-20 of the deviation the rest may come from the roundings of the differences
+    // and of their sum, and near zero the first sum is the more exact one (bf16 4096 columns around
+    // 0: the mean off by 4e-8 of itself, 1.5e-6 with the rest on top).
+    __device__ __forceinline__ float full_mean(float m) const { return mean * mean <= least ? m : m + mean; }
 };
 
 // Sum over a workgroup of 256 threads, in every thread. `part`: 4 values of LDS.
@@ -60,23 +70,26 @@ __global__ __launch_bounds__(256) void norm_rows(NormArgs<T> a) {
             for (int e = 0; e < n; ++e) s += v.at(e);
         }
         const float m = block_sum(s, part) / (float)a.cols;
-        float sd = 0.f, sq = 0.f;
+        double all = 0.;                     // of any number of vectors
+        float sq = 0.f;
         for (int64_t c = (int64_t)threadIdx.x * n; c < a.cols; c += 256 * n) {
             Vec<T> v;
             const int valid = inside(a.cols, c, n);
             v.load(x + c, valid);
+            float sd = 0.f;
 #pragma unroll
             for (int e = 0; e < n; ++e) {
                 const float d = v.at(e) - m;
                 sd += e < valid ? d : 0.f;
                 sq += e < valid ? d * d : 0.f;
             }
+            all += (double)sd;
         }
-        sd = block_sum(sd, part);
-        const Rest rest(sd, block_sum(sq, part), 1.f / (float)a.cols, a.eps);
+        const float sd = block_sum((float)all, part) / (float)a.cols;
+        const Rest rest(sd, block_sum(sq, part) / (float)a.cols, a.eps);
         const float r = rest.rstd, shift = -rest.mean * r;
         if (threadIdx.x == 0) {
-            if (a.mean != nullptr) a.mean[row] = m + rest.mean;
+            if (a.mean != nullptr) a.mean[row] = rest.full_mean(m);
             if (a.rstd != nullptr) a.rstd[row] = r;
         }
         for (int64_t c = (int64_t)threadIdx.x * n; c < a.cols; c += 256 * n) {
@@ -145,9 +158,7 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm(NormArgs<T> a, float i
 #pragma unroll
         for (int q = 0; q < kWaves; ++q) s += part[t / L * kWaves + q];
     }
-    // s / columns, as rounded: the rest of the first quotient is exact.
-    float m = s * inv;
-    m = __builtin_fmaf(__builtin_fmaf(-m, (float)cols, s), inv, m);
+    const float m = over_cols(s, (float)cols, inv);
     float sd = 0.f, sq = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -174,11 +185,11 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm(NormArgs<T> a, float i
             sq += parts[t / L * kWaves + q].y;
         }
     }
-    const Rest rest(sd, sq, inv, a.eps);
+    const Rest rest(sd * inv, over_cols(sq, (float)cols, inv), a.eps);
     const float r = rest.rstd, shift = -rest.mean * r;
     if (!on) return;
     if (lane == 0) {
-        if (a.mean != nullptr) a.mean[row] = m + rest.mean;
+        if (a.mean != nullptr) a.mean[row] = rest.full_mean(m);
         if (a.rstd != nullptr) a.rstd[row] = r;
     }
     if constexpr (kLate) load_columns();

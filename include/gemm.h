@@ -503,9 +503,9 @@ gemm_status_t gemm_bf16_grouped_wgrad_f32(int64_t groups, int64_t M, int64_t N, 
  * rounding. A row that holds an infinity or a NaN gets NaN; one whose sum, or whose
  * sum of the squares (x - m)^2, passes fp32's range gets NaN or r = 0. The
  * differences are taken from a first mean, and their own mean is taken off them, so Y
- * and rstd of rows far from zero lose nothing. mean is rounded to fp32, and the
- * gradient takes that: its (x - m) r are off by up to half a step of the mean
- * times r (mean 4096, deviation 1: 2.4e-4). rows == 0 or cols == 0 does nothing. */
+ * and rstd of rows far from zero lose nothing. mean is one fp32 value, and the
+ * gradient takes that: its (x - m) r are off by up to 2^-20 and half a step of the
+ * mean times r (mean 4096, deviation 1: 2.4e-4). rows == 0 or cols == 0 does nothing. */
 gemm_status_t gemm_layernorm_bf16(int64_t rows, int64_t cols, float eps, const uint16_t* X, int64_t ldx,
                                   const uint16_t* weight, const uint16_t* bias, uint16_t* Y, int64_t ldy,
                                   float* mean, float* rstd, void* stream);

@@ -84,3 +84,16 @@ def test_rows_whose_weight_comes_late(cols):
         assert worst(y, norm_ref(*args)[0], norm_allow(*args, BF16)[0]) <= 1
     dg.layernorm(x, x)
     assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("cols", COLS)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_means_of_exact_sums(cols, dtype):
+    """Multiples of 2^-7 up to 1: every partial sum is below 2^24 of them, so exact, and the mean is a
+    quotient off by a step, however near zero it lies."""
+    for rows in (5, 600 if cols <= 9000 else 7):
+        x = (torch.randint(-128, 129, (rows, cols), generator=gen(cols)) / 128).to(dtype)
+        mean = torch.empty(rows, device="cuda")
+        dg.layernorm(x.cuda(), torch.empty_like(x, device="cuda"), None, None, 1e-5, mean)
+        want = f64(x).mean(1)
+        assert worst(mean, want, 2 * U * np.abs(want)) <= 1
