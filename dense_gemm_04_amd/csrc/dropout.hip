@@ -7,7 +7,7 @@
 // chance to be dropped is a multiple of 2^-16, and the factor of what is kept is
 // exactly its inverse, so that the mean is kept too.
 //
-// Bound by memory: 8192 x 4096 bf16 with a residual 37 us (5.4 TB/s), of which the
+// Bound by memory: 8192 x 4096 bf16 with a residual 38 us (5.3 TB/s), of which the
 // 180 vector instructions a thread, mostly the generator's, fill 19.
 
 #include "layer.hpp"
@@ -33,7 +33,7 @@ __device__ __forceinline__ u32x4 philox(uint32_t c0, uint32_t c1, uint32_t c2, u
 
 // A vector of 16 bytes to a thread, so that a wave reads and writes whole
 // stretches: in fp32 two threads draw the same numbers and use half of them each
-// (4095 x 1023 in fp32: 8.0 us, 9.2 with 8 columns to a thread, 32 bytes from lane to
+// (4095 x 1023 in fp32: 7.7 us, 9.0 with 8 columns to a thread, 32 bytes from lane to
 // lane). I: the type that counts vectors.
 template <typename T, typename I>
 __global__ __launch_bounds__(256) void dropout(DropoutArgs<T> a, float scale, I vecs, I all) {

@@ -14,9 +14,9 @@
 // are not whole vectors read their last n columns again, at whatever alignment,
 // and count each once.
 //
-// One MI355X: the norm of 8192 x 4096 bf16 25 us (5.4 TB/s; a copy of as much
-// 26.5), its gradients with a residual 53 us and 5 for the last sums (5.0 TB/s over
-// all); 262144 x 128 bf16 23 and 39 us; 16 x 8192 bf16 3.5 us.
+// One MI355X: the norm of 8192 x 4096 bf16 26 us (5.2 TB/s; a copy of as much
+// 26.5), its gradients with a residual 52 us and 5 for the last sums (4.7 TB/s over
+// all); 262144 x 128 bf16 28 and, with a residual, 52 us; 16 x 8192 bf16 3.6 us.
 
 #include "layer.hpp"
 
@@ -264,7 +264,7 @@ __device__ __forceinline__ void add_to(float* out, float beta, float v) {
 // since a column may have millions of terms (262144 x 5: fp32 chains of 65536 were off by
 // more than 3 steps of the terms' sum). Slices leave theirs in the workspace, P values
 // of dweight and P of dbias each. 262144 x 5 bf16 0.58 ms with both kernels, 11 in one
-// slice; 1024 x 40000 117 us, 167 with a row at a time.
+// slice; 1024 x 40000 without R 114 us, 190 with a row at a time.
 template <typename T, int P>
 __global__ __launch_bounds__(256) void norm_grad_cols(NormGradArgs<T> a) {
     constexpr int kRows = 256 / P;
@@ -334,7 +334,7 @@ inline int slices_of(int64_t rows, int64_t cols) {
 // waves), V vectors to a thread, which keeps the row's values in registers
 // between the row's sums and dX, and its columns' sums of dY h and dY in 2 V n
 // more. PRE: the next row is on its way meanwhile (8192 x 4096 bf16 with a residual:
-// 53 us with 32 values of a row to a thread and the next one on its way, 62 with 64
+// 52 us with 32 values of a row to a thread and the next one on its way, 62 with 64
 // and without). A workgroup of 512 threads takes
 // 512 / L rows at a time and adds its threads' column sums up in LDS at the end,
 // into one image of the registers for each workgroup; sum_images adds those.
@@ -589,6 +589,10 @@ __global__ __launch_bounds__(256) void sum_images(const f32x4* images, int count
 // Threads to a row and vectors to a thread: 16 lanes up to 16 vectors; then as few
 // waves as hold the row in 32 values a thread; up to 64 in 8 waves. 0 threads: no such
 // kernel (rows shorter than a vector, or longer than 32768 values in bf16, 16384 in fp32).
+// Above 20480 values of bf16 registers spill. With a residual, 1024 rows of 20480, 24576, 28672 and
+// 32768 take 58, 72, 111 and 154 us, the general kernels 84, 92, 100 and 107; 16 rows 13, 15, 19
+// and 23 against 21, 24, 28 and 31; 4096 rows 148, 183, 338 and 456 against 320, 365, 411 and 452.
+// fp32 does not spill (1024 x 16384 75 us, 104).
 struct Width {
     int lanes, vecs;
 };
@@ -603,8 +607,9 @@ inline Width width_of(int64_t cols, int n) {
 
 constexpr int64_t kManyRows = 512;
 constexpr int kImages = 256;        // workgroups of norm_grad: one to a compute unit
-// One alone up to two turns: a second launch costs more than the second turn (16 x
-// 1024 bf16 5.5 us, 7.5 with two launches; 16 x 4096 8.8 and 9.4).
+// One alone up to two turns, where a second launch costs as much as the second turn
+// or more, and a call less (bf16, two turns, alone and in two launches: 64 x 64 4.8
+// and 6.0 us, 16 x 1024 5.8 and 6.8, 8 x 4096 9.05 and 9.0; four turns: 16 x 4096 14.1 and 9.1).
 inline int64_t grad_blocks(int64_t rows, const Width& w) {
     const int groups = 512 / w.lanes;
     if (rows <= 2 * groups) return 1;

@@ -25,7 +25,7 @@
 // execution.
 //
 // Neither memory nor the vector unit bounds it, but the way through both: 16384
-// tokens x 128 experts, 8 choices 8.8 us (4 of them vector instructions) and 6.7
+// tokens x 128 experts, 8 choices 8.5 us (4 of them vector instructions) and 6.9
 // for 10 MB, 16 x 32, 2 choices 4.5, the gradient of 8191 x 64 3.8.
 
 #include "layer.hpp"

@@ -7,10 +7,17 @@
 //     gradient  dY(slot_tj) = gate_tj dC(t),  dgate_tj = dC(t) . Y(slot_tj)
 //
 // Bound by memory. A token's k slots are read first and held in scalar registers
-// (K: k rounded up to a power of two), so that the k rows' loads leave
-// together. One MI355X: gather of 8191 x 4096, 2 choices 38.9 us (5.2 TB/s),
+// (K: k rounded up to a power of two), so that the k rows' loads of whole vectors
+// leave together. One MI355X: gather of 8191 x 4096, 2 choices 38.6 us (5.2 TB/s),
 // combine of 4096 x 2048, 8 choices 29.4 (5.7), its gradient of 8192 x 4096, 2
 // choices 64 (5.3).
+//
+// Where that does not hold: a row's last, partial vector is read element by
+// element, one choice after the other (4096 x 2047, 8 choices: gather 45 us, combine 51,
+// gradient 117, against 32, 30 and 63 for 2048 columns); combine of more than 8
+// choices keeps its rows in private memory (4096 x 2048, 16 choices 147 us, its
+// bytes 60); and rows much narrower than the 2048 columns of a workgroup leave
+// threads idle (16384 x 256, 8 choices: 28, 35 and 86 us for bytes of 15, 17 and 28).
 
 #include "layer.hpp"
 

@@ -487,7 +487,7 @@ gemm_status_t gemm_bf16_grouped_wgrad_f32(int64_t groups, int64_t M, int64_t N, 
  * order and back, with their gradients. Matrices are row-major with a leading
  * dimension as everywhere here; every alignment is taken, and rows on 16 bytes
  * are the fastest. Everything between the operands and a result is formed in
- * fp32 and rounded once. The same call gives the same bits.
+ * fp32, or in 64 bits, and rounded once. The same call gives the same bits.
  * Streams, errors and ownership are those of the other calls. An output may be
  * the same matrix (base and leading dimension) as an input only where said;
  * other overlaps give undefined results.
@@ -628,7 +628,9 @@ gemm_status_t gemm_moe_route_grad_f32(int64_t tokens, int64_t experts, int k, in
  *
  * The gradient of gather is combine with gates NULL (1). An absent slot's term is
  * 0 * gates[t,j] (so that a router's NaN shows) and its dgates 0. R may be NULL, and C may be R.
- * dgates may be NULL, and then Y too; with gates NULL dY takes dC itself. dY may be Y.
+ * dgates may be NULL, and then Y too; with gates NULL dY takes dC itself. Of two
+ * equal slots each column of dY keeps either's value. dY may be Y if no two slots
+ * are equal (moe_route's never are).
  * k terms are summed in the order of j. */
 gemm_status_t gemm_moe_gather_bf16(int64_t tokens, int k, int64_t cols, int64_t rows, const uint16_t* X,
                                    int64_t ldx, const int32_t* slots, uint16_t* Y, int64_t ldy, void* stream);
